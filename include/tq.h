@@ -23,7 +23,7 @@
  *     returned before anything is launched; nothing is written in that case.
  *   - The caller allocates and owns every buffer.  The library never allocates or
  *     frees device memory; the one device memory it keeps is the fixed scratch array
- *     of tq_attend_static (declared last), which exists only for that call.
+ *     of tq_attend_static (declared below), which exists only for that call.
  *   - Device work is enqueued asynchronously on the caller's stream; results are
  *     ready when that stream is synchronised.  Outputs are bit-identical run to run.
  *   - Device pointers must be 16-byte aligned (TQ_ERR_INVALID_ARG otherwise).
@@ -60,7 +60,8 @@ typedef enum tq_status {
     TQ_ERR_TIMEOUT = 4      /* a bounded device-side wait gave up (dev_status)    */
 } tq_status;
 
-typedef enum tq_dtype { TQ_F16 = 0, TQ_F32 = 1 } tq_dtype;
+/* TQ_BF16 (bfloat16): queries and outputs of tq_attend_shared and tq_attend_weigh only. */
+typedef enum tq_dtype { TQ_F16 = 0, TQ_F32 = 1, TQ_BF16 = 2 } tq_dtype;
 
 /* Human-readable name of a status code.  Never returns NULL. */
 const char *tq_status_string(int status);
@@ -345,6 +346,87 @@ tq_status tq_attend_static(const tq_params *p, const float *q, int B, int Hq, in
                            const uint32_t *kcodes, const uint32_t *ksigns, const uint16_t *knorm,
                            const uint16_t *krnorm, const uint32_t *vcodes, const uint16_t *vnorm,
                            float scale, float *out, int32_t *dev_status, tq_stream_t stream);
+
+/*
+ * tq_attend_shared -- attention of a batch whose sequences continue one shared context.
+ * (The pages have no counterpart: this is an addition of the library.)
+ * The records of the shared prefix are stored once and read once for the whole batch; every
+ * sequence's own tokens follow in its own cache, as many as lens says.  With the estimates s_t of
+ * tq_scores and the dequantized values v_t of tq_attend,
+ *   out = sum_t softmax_t(scale * s_t) v_t  over the prefix and the first lens[b] own tokens.
+ * A sequence with nothing to attend gets zeros.
+ *   q        : device [B, Hq, Nq, dim] of dtype: TQ_F16, TQ_BF16 or TQ_F32
+ *   t_prefix : tokens of the prefix, >= 0; its arrays hold Hkv * t_prefix records, [Hkv, t_prefix]
+ *              (NULL when t_prefix is 0)
+ *   lens     : device int32 [B], tokens in each sequence's own cache, 0 .. t_cap.  Read when the
+ *              work runs, so that a captured graph follows its changes.  A value outside is taken
+ *              as the nearest one inside, and TQ_ERR_INVALID_ARG is set in dev_status
+ *   t_cap    : capacity of the own caches, >= 0: B * Hkv * t_cap records, [B, Hkv, t_cap] (arrays
+ *              and lens NULL when t_cap is 0).  t_prefix + t_cap >= 1.  Records behind lens[b] are
+ *              not used
+ *   scale    : as tq_attend
+ *   out      : device [B, Hq, Nq, dim] of dtype
+ *   scratch  : tq_attend_shared_scratch_bytes(...) bytes; calls that share it must not overlap
+ * Precision: with TQ_F32 the products keep 32 bits.  With the 16-bit types the operands of a
+ * product are rounded to 16 bits (relative 2^-11) and sums, maxima and normalisers are in 32.
+ * TQ_ERR_UNSUPPORTED when t_prefix or t_cap exceeds 2^31 - 64 or B * Hq * Nq exceeds 2^18.
+ */
+size_t tq_attend_shared_scratch_bytes(const tq_params *p, tq_dtype dtype, int B, int Hq, int Hkv, int Nq,
+                                      int64_t t_prefix, int64_t t_cap);
+tq_status tq_attend_shared(const tq_params *p, const void *q, tq_dtype dtype, int B, int Hq, int Hkv, int Nq,
+                           int64_t t_prefix, const uint32_t *pkcodes, const uint32_t *pksigns,
+                           const uint16_t *pknorm, const uint16_t *pkrnorm, const uint32_t *pvcodes,
+                           const uint16_t *pvnorm, const int32_t *lens, int64_t t_cap, const uint32_t *kcodes,
+                           const uint32_t *ksigns, const uint16_t *knorm, const uint16_t *krnorm,
+                           const uint32_t *vcodes, const uint16_t *vnorm, float scale, void *out, void *scratch,
+                           size_t scratch_bytes, int32_t *dev_status, tq_stream_t stream);
+
+/*
+ * tq_attend_weigh -- attention over caches of different lengths that also adds up how much weight
+ * each cached token got, which tq_evict goes by.
+ * (The pages have no counterpart: this is an addition of the library.)
+ *   out                  as tq_attend_shared without a prefix
+ *   weights[b, h, t] +=  sum over the Hq/Hkv * Nq query rows of KV head h of softmax_t(scale * s_t),
+ *                        for t < lens[b]; entries behind are left as they are
+ *   weights : device fp32 [B, Hkv, t_cap]
+ * The other arguments are those of tq_attend_shared; t_cap >= 1.  The scores behind the weights
+ * keep 32 bits whatever dtype is.  The rows are added in ascending order: results are bit-identical
+ * run to run.
+ *   scratch : tq_attend_weigh_scratch_bytes(...) bytes, among them 4 for each (query row, slot)
+ */
+size_t tq_attend_weigh_scratch_bytes(const tq_params *p, tq_dtype dtype, int B, int Hq, int Hkv, int Nq,
+                                     int64_t t_cap);
+tq_status tq_attend_weigh(const tq_params *p, const void *q, tq_dtype dtype, int B, int Hq, int Hkv, int Nq,
+                          const int32_t *lens, int64_t t_cap, const uint32_t *kcodes, const uint32_t *ksigns,
+                          const uint16_t *knorm, const uint16_t *krnorm, const uint32_t *vcodes,
+                          const uint16_t *vnorm, float scale, float *weights, void *out, void *scratch,
+                          size_t scratch_bytes, int32_t *dev_status, tq_stream_t stream);
+
+/*
+ * tq_evict -- copy each slice's heaviest tokens into another (smaller) cache.
+ * (The pages have no counterpart: this is an addition of the library.)
+ * Of the n = lens[b] tokens of a (batch, KV head) slice, min(n, budget) are kept: the last
+ * `recent` ones always, then those of the largest weights, ties to the smaller slot.  They keep
+ * their order.  The packed records are copied as they are, the weights with them.
+ *   lens, t_cap : as tq_attend_weigh, for the source arrays and weights
+ *   weights     : device fp32 [B, Hkv, t_cap].  A NaN counts as heavier than any number
+ *   budget      : 1 .. t_cap;  recent: 0 .. budget
+ *   out_cap     : capacity of the destination, >= budget: [B, Hkv, out_cap] records and weights.
+ *                 Slots behind the kept tokens are left as they are.  The destination must not
+ *                 overlap the source (TQ_ERR_INVALID_ARG)
+ *   kept        : device int32 [B, Hkv, budget], the kept slots in ascending order; entries behind
+ *                 the last one are left as they are
+ *   out_lens    : device int32 [B], min(n, budget); must not be lens
+ *   scratch     : tq_evict_scratch_bytes(...) bytes
+ */
+size_t tq_evict_scratch_bytes(const tq_params *p, int B, int Hkv, int64_t t_cap, int64_t budget);
+tq_status tq_evict(const tq_params *p, int B, int Hkv, const int32_t *lens, int64_t t_cap, const uint32_t *kcodes,
+                   const uint32_t *ksigns, const uint16_t *knorm, const uint16_t *krnorm, const uint32_t *vcodes,
+                   const uint16_t *vnorm, const float *weights, int64_t budget, int64_t recent, int64_t out_cap,
+                   uint32_t *out_kcodes, uint32_t *out_ksigns, uint16_t *out_knorm, uint16_t *out_krnorm,
+                   uint32_t *out_vcodes, uint16_t *out_vnorm, float *out_weights, int32_t *kept,
+                   int32_t *out_lens, void *scratch, size_t scratch_bytes, int32_t *dev_status,
+                   tq_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -34,7 +34,7 @@ def _stale() -> bool:
 
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     if force or verbose_ptxas or _stale():
-        cmd = [NVCC, *ARCH, *FLAGS]
+        cmd = [NVCC, *ARCH, *FLAGS, "--threads", "0"]
         if verbose_ptxas:
             cmd += ["-Xptxas", "-v"]
         cmd += ["-o", LIB, *sources()]

@@ -1,0 +1,154 @@
+// tq_serve.cuh -- what the kernels of tq_attend_shared and tq_attend_weigh share: the problem, the
+// division of ragged contexts among CTAs, the scratch layout and the launchers.
+//
+// Estimated logits of query row r against token t, in log2 units:
+//   z = f_r ||k_t|| ( sum_j Q_rj C[kidx_tj] + rho_t sum_i P_ri sgn_ti )
+// Q = sigma 2^-e_r R q, P = 2^-e_r sqrt(pi/2)/m S q, C[k] = c[k] / sigma and
+// f_r = 2^e_r scale log2(e): sigma is a scale of the codebook (below), e_r one of the row, both
+// chosen so that 16-bit operands lose nothing they need.
+//
+// Softmax with the value norms inside.  With y = z + log2 ||v_t|| and a running reference
+// N >= y - 8 the weights w = 2^(y - N) are what multiplies the value centroids, and the
+// normaliser is l = sum w / ||v_t||; both have the factor 2^-N, so
+//   out = R^T (sum_t w_t c[vidx_t]) / l
+// needs no product with ||v_t|| and w stays inside the range of 16-bit floats whatever the norms
+// are (||v_t|| is taken as 2^-24, fp16's smallest number, where it is 0, with c as 0).
+// A partial result of a row is (N, l, o = sum_t w_t c[vidx_t]); partials merge by their N.
+#pragma once
+
+#include "tq_common.cuh"
+#include "tq_internal.cuh"
+
+namespace tq {
+
+constexpr int kStage = 32;       // tokens of one copy stage: the unit in which contexts are divided
+constexpr float kMinNorm = 5.9604644775390625e-8f;  // 2^-24
+constexpr float kLog2eF = 1.4426950408889634f;
+
+__host__ __device__ constexpr int partial_stride(int d) { return d + 4; }  // (N, l, -, -, o[d])
+
+// 16-bit operand tables of one call (fp16 bits), written by the preparation kernel.
+struct ServeTables {
+    uint16_t kh[8], kl[8];    // c_k / sigma = kh + kl for the keys' codebook
+    uint16_t vh[16], vl[16];  // c_v / tau = vh + vl for the values'
+    float tau;                // a power of two
+    float pad[3];
+};
+
+// The caches of one attention pass.  `slices` slices of records, `stride` records apart; slice s
+// belongs to sequence s / per_seq and holds len[s / per_seq] tokens.  A slice is attended by
+// `rows` query rows, of which row r is row (r / rows_in) * rows_outer + s * rows_in + r % rows_in
+// of the call's queries [B, Hkv, rows_in].
+struct RaggedCache {
+    const uint32_t *kcodes, *ksigns;
+    const uint16_t *knorm, *krnorm;
+    const uint32_t *vcodes;
+    const uint16_t *vnorm;
+    int64_t stride, records;  // records of the whole array (no read goes past it)
+    int slices, per_seq, nseq;
+    int rows, rows_in;
+    int64_t rows_outer;
+    const int32_t *len;  // device, [nseq], within [0, stride]
+    const int64_t *cum;  // device, [nseq + 1]: stages of the sequences before (of one slice each)
+    int ctas;            // CTAs the stages of all slices are divided among
+};
+
+__device__ __forceinline__ int64_t ragged_row(const RaggedCache &c, int slice, int r) {
+    return (int64_t)(r / c.rows_in) * c.rows_outer + (int64_t)slice * c.rows_in + r % c.rows_in;
+}
+
+// The W stages of all slices, in order, are divided evenly among G = min(ctas, W) CTAs, so that none
+// of these is without work; CTA i takes stages [i W / G, (i + 1) W / G) and so a piece of one or
+// more slices.  Slice s's piece in CTA i has the partial number i + s: from one piece to the next
+// either i or s grows, so no two pieces share one.
+struct Piece {
+    int slice;
+    int64_t s0, s1;  // stages of the slice
+    int len;         // tokens of the slice
+};
+
+__device__ __forceinline__ int64_t ragged_total(const RaggedCache &c) { return c.cum[c.nseq] * c.per_seq; }
+__device__ __forceinline__ int64_t cta_first(int64_t total, int ctas, int i) {
+    const int64_t g = total < ctas ? total : ctas;
+    return i >= g ? total : total * i / g;
+}
+
+// The piece that starts at stage w (< w1) of the division.
+__device__ __forceinline__ Piece piece_at(const RaggedCache &c, int64_t w, int64_t w1) {
+    int lo = 0, hi = c.nseq - 1;  // the last sequence whose first stage is <= w and that has stages
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (c.cum[mid] * c.per_seq <= w) lo = mid;
+        else hi = mid - 1;
+    }
+    const int64_t base = c.cum[lo] * c.per_seq, n = c.cum[lo + 1] - c.cum[lo];
+    const int64_t h = (w - base) / n;
+    Piece p;
+    p.slice = (int)(lo * (int64_t)c.per_seq + h);
+    p.s0 = w - base - h * n;
+    const int64_t left = w1 - w;
+    p.s1 = p.s0 + left < n ? p.s0 + left : n;
+    p.len = c.len[lo];
+    return p;
+}
+
+// The CTAs [first, last] that hold pieces of a slice; false when the slice is empty.
+__device__ __forceinline__ bool slice_ctas(const RaggedCache &c, int slice, int *first, int *last) {
+    const int b = slice / c.per_seq;
+    const int64_t n = c.cum[b + 1] - c.cum[b];
+    if (n == 0) return false;
+    const int64_t total = ragged_total(c), g = total < c.ctas ? total : c.ctas;
+    const int64_t w0 = c.cum[b] * c.per_seq + (int64_t)(slice - b * c.per_seq) * n, w1 = w0 + n - 1;
+    // CTA i holds w exactly when floor(W i / G) <= w < floor(W (i + 1) / G)
+    *first = (int)(((w0 + 1) * g - 1) / total);
+    *last = (int)(((w1 + 1) * g - 1) / total);
+    return true;
+}
+
+// One call of tq_attend_shared or tq_attend_weigh.
+struct ServeCall {
+    Prepared P;
+    const void *q;
+    void *out;
+    tq_dtype dtype;
+    int B, Hq, Hkv, Nq;
+    int64_t rows;  // B * Hq * Nq
+    float scale;
+    RaggedCache own, prefix;  // prefix.slices == 0: none; own.slices == 0: none
+    const int32_t *lens;      // the caller's, device
+    int64_t t_cap, t_prefix;
+    float *weights;           // tq_attend_weigh
+    int32_t *dev_status;
+};
+
+// How a call is computed: by sizes alone, so that the scratch size follows from them too.
+struct ServePlan {
+    bool fast;         // the tensor-core kernels (else the plain kernel)
+    int row_block;     // query rows a CTA of the ragged kernel takes
+    int own_ctas;      // division of the own caches (0: no own caches)
+    int prefix_ctas;   // division of the prefix by the ragged kernel (0: not by it)
+    // byte offsets in the scratch
+    size_t tables, lens, cum, qprep, fscale, zbuf, lse, own_part, pre_part, total;
+};
+
+ServePlan plan_serve(const Prepared &P, tq_dtype dtype, int B, int Hq, int Hkv, int Nq, int64_t t_prefix,
+                     int64_t t_cap, bool weigh);
+cudaError_t launch_serve(const ServeCall &call, const ServePlan &plan, void *scratch, cudaStream_t s);
+
+// Pieces of a launch_serve (each in its file)
+struct RaggedArgs {
+    Prepared P;
+    RaggedCache c;
+    const ServeTables *tables;
+    const float *qprep;   // [rows, d + m], (Q, P) of each row
+    const float *fscale;  // [rows]
+    float *part;          // partials, [(ctas + slices) * c.rows, d + 4]
+    float *zbuf;          // z of every (row of the slice, token): [slices, rows, stride], or null
+};
+cudaError_t launch_ragged_plain(const RaggedArgs &a, cudaStream_t s);
+bool ragged_mma_supported(const Prepared &P);
+int ragged_mma_rows(const Prepared &P, bool f32, int rows);  // the row block for so many rows a slice
+int ragged_mma_ctas_per_sm(const Prepared &P);
+cudaError_t launch_ragged_mma(const RaggedArgs &a, bool f32, int row_block, cudaStream_t s);
+
+}  // namespace tq

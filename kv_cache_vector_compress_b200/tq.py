@@ -24,7 +24,7 @@ if not os.path.exists(LIB_PATH):
 _lib = ctypes.CDLL(LIB_PATH)
 
 TQ_OK, TQ_ERR_INVALID_ARG, TQ_ERR_UNSUPPORTED, TQ_ERR_CUDA, TQ_ERR_TIMEOUT = 0, 1, 2, 3, 4
-TQ_F16, TQ_F32 = 0, 1
+TQ_F16, TQ_F32, TQ_BF16 = 0, 1, 2
 
 
 class tq_params(ctypes.Structure):
@@ -84,6 +84,21 @@ _lib.tq_attend_merge.restype = _I
 _lib.tq_attend_static.argtypes = [_PP, _P, _I, _I, _I, _I, _I64, _P, _P, _P, _P, _P, _P, ctypes.c_float, _P,
                                   _P, _P]
 _lib.tq_attend_static.restype = _I
+_lib.tq_attend_shared_scratch_bytes.argtypes = [_PP, _I, _I, _I, _I, _I, _I64, _I64]
+_lib.tq_attend_shared_scratch_bytes.restype = _SZ
+_lib.tq_attend_shared.argtypes = [_PP, _P, _I, _I, _I, _I, _I, _I64, _P, _P, _P, _P, _P, _P, _P, _I64, _P, _P, _P, _P,
+                                  _P, _P, ctypes.c_float, _P, _P, _SZ, _P, _P]
+_lib.tq_attend_shared.restype = _I
+_lib.tq_attend_weigh_scratch_bytes.argtypes = [_PP, _I, _I, _I, _I, _I, _I64]
+_lib.tq_attend_weigh_scratch_bytes.restype = _SZ
+_lib.tq_attend_weigh.argtypes = [_PP, _P, _I, _I, _I, _I, _I, _P, _I64, _P, _P, _P, _P, _P, _P, ctypes.c_float, _P, _P,
+                                 _P, _SZ, _P, _P]
+_lib.tq_attend_weigh.restype = _I
+_lib.tq_evict_scratch_bytes.argtypes = [_PP, _I, _I, _I64, _I64]
+_lib.tq_evict_scratch_bytes.restype = _SZ
+_lib.tq_evict.argtypes = [_PP, _I, _I, _P, _I64, _P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _P, _P, _P, _P, _P, _P,
+                          _P, _P, _P, _P, _SZ, _P, _P]
+_lib.tq_evict.restype = _I
 _lib.tq_selftest_wait_timeout.argtypes = [_P, ctypes.c_uint32, _P]
 _lib.tq_selftest_wait_timeout.restype = _I
 
@@ -98,7 +113,9 @@ EXPORTS = ["tq_status_string", "tq_version", "tq_codebook", "tq_codebook_beta", 
            "tq_attend_scratch_bytes", "tq_attend", "tq_attend_partial", "tq_attend_merge", "tq_append_attend",
            "tq_compress_attend_host_scratch_bytes", "tq_compress_attend_host",
            "tq_selftest_wait_timeout",
-           "tq_attend_static"]
+           "tq_attend_static",
+           "tq_attend_shared_scratch_bytes", "tq_attend_shared", "tq_attend_weigh_scratch_bytes", "tq_attend_weigh",
+           "tq_evict_scratch_bytes", "tq_evict"]
 
 
 class TQError(RuntimeError):
@@ -388,3 +405,159 @@ def tq_selftest_wait_timeout(dev_status: torch.Tensor, timeout_ms: int = 100):
     limit, which must leave TQ_ERR_TIMEOUT in dev_status (a device int32 tensor)."""
     _check(_lib.tq_selftest_wait_timeout(_ptr(dev_status), timeout_ms, _stream()), "tq_selftest_wait_timeout")
 
+
+_ROW_DTYPES = {torch.float16: TQ_F16, torch.float32: TQ_F32, torch.bfloat16: TQ_BF16}
+
+
+def _row_dtype(dtype: torch.dtype) -> int:
+    if dtype not in _ROW_DTYPES:
+        raise TypeError("q must be float16, bfloat16 or float32")
+    return _ROW_DTYPES[dtype]
+
+
+def _need(t, name: str, dtype: torch.dtype, n: int, dev: torch.device):
+    """Raise unless t is a tensor of dtype with n values on the device of the other tensors."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}")
+    if t.numel() != n:
+        raise ValueError(f"{name} must hold {n} values, not {t.numel()}")
+    if t.device != dev:
+        raise ValueError(f"{name} must be on {dev}")
+
+
+def _on_current(p: Params, dev: torch.device):
+    if dev.type != "cuda" or dev.index != torch.cuda.current_device() or p.workspace.device != dev:
+        raise ValueError("the tensors and the parameter set must be on the current CUDA device")
+
+
+def _need_cache(p: Params, keys, values, n: int, what: str, dev: torch.device):
+    """Check a cache of n records (keys: codes, signs, norm, rnorm; values: codes, norm)."""
+    kc, ks, kn, kr = keys
+    vc, vn = values
+    _need(kc, f"{what} key codes", torch.int32, n * p.key_words(), dev)
+    _need(ks, f"{what} key signs", torch.int32, n * (p.proj_dim // 32), dev)
+    _need(kn, f"{what} key norms", torch.float16, n, dev)
+    _need(kr, f"{what} key residual norms", torch.float16, n, dev)
+    _need(vc, f"{what} value codes", torch.int32, n * p.value_words(), dev)
+    _need(vn, f"{what} value norms", torch.float16, n, dev)
+
+
+def _need_rest(p: Params, q, out, scratch, need: int, dev_status):
+    _need(out, "out", q.dtype, q.numel(), q.device)
+    if scratch.device != q.device or scratch.numel() * scratch.element_size() < need:
+        raise ValueError(f"scratch must hold {need} bytes on {q.device}")
+    if dev_status is not None:
+        _need(dev_status, "dev_status", torch.int32, 1, q.device)
+
+
+def tq_attend_shared_scratch_bytes(p: Params, dtype: torch.dtype, B, Hq, Hkv, Nq, t_prefix, t_cap) -> int:
+    return _lib.tq_attend_shared_scratch_bytes(p.ref, _row_dtype(dtype), B, Hq, Hkv, Nq, t_prefix, t_cap)
+
+
+def tq_attend_shared(p: Params, q: torch.Tensor, prefix_keys, prefix_values, keys, values, lens, Hkv: int,
+                     t_prefix: int, t_cap: int, scale: float = 0.0, out=None, scratch=None, dev_status=None):
+    """Attention of q [B, Hq, Nq, dim] (float16, bfloat16 or float32; the output has its type) over a
+    compressed prefix that the whole batch shares (records [Hkv, t_prefix]) and the first lens[b]
+    tokens (int32 [B]) of each sequence's own cache (records [B, Hkv, t_cap]).  The prefix tuples are
+    None when t_prefix is 0; the own ones and lens when t_cap is 0."""
+    B, Hq, Nq, d = q.shape
+    dt, dev = _row_dtype(q.dtype), q.device
+    _on_current(p, dev)
+    if d != p.dim:
+        raise ValueError(f"q must have {p.dim} coordinates")
+    if t_prefix > 0:
+        _need_cache(p, prefix_keys, prefix_values, Hkv * t_prefix, "prefix", dev)
+    if t_cap > 0:
+        _need_cache(p, keys, values, B * Hkv * t_cap, "own", dev)
+        _need(lens, "lens", torch.int32, B, dev)
+    need = tq_attend_shared_scratch_bytes(p, q.dtype, B, Hq, Hkv, Nq, t_prefix, t_cap)
+    if out is None:
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    if scratch is None:
+        scratch = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+    _need_rest(p, q, out, scratch, need, dev_status)
+    pre = [_ptr(t) for t in (*prefix_keys, *prefix_values)] if t_prefix > 0 else [None] * 6
+    own = [_ptr(t) for t in (*keys, *values)] if t_cap > 0 else [None] * 6
+    _check(_lib.tq_attend_shared(p.ref, _ptr(q), dt, B, Hq, Hkv, Nq, t_prefix, *pre, _ptr(lens if t_cap > 0 else None),
+                                 t_cap, *own, float(scale), _ptr(out), _ptr(scratch), scratch.numel() * scratch.element_size(),
+                                 _ptr(dev_status), _stream()), "tq_attend_shared")
+    return out
+
+
+def tq_attend_weigh_scratch_bytes(p: Params, dtype: torch.dtype, B, Hq, Hkv, Nq, t_cap) -> int:
+    return _lib.tq_attend_weigh_scratch_bytes(p.ref, _row_dtype(dtype), B, Hq, Hkv, Nq, t_cap)
+
+
+def tq_attend_weigh(p: Params, q: torch.Tensor, keys, values, lens: torch.Tensor, Hkv: int, t_cap: int,
+                    weights: torch.Tensor, scale: float = 0.0, out=None, scratch=None, dev_status=None):
+    """Attention of q [B, Hq, Nq, dim] (float16, bfloat16 or float32) over the first lens[b] tokens of
+    each sequence's cache (records [B, Hkv, t_cap]).  Adds to weights (float32 [B, Hkv, t_cap], in
+    place) the softmax weight every token got, summed over the query rows of its KV head.  Returns
+    the output, of q's type."""
+    B, Hq, Nq, d = q.shape
+    dt, dev = _row_dtype(q.dtype), q.device
+    _on_current(p, dev)
+    if d != p.dim:
+        raise ValueError(f"q must have {p.dim} coordinates")
+    _need_cache(p, keys, values, B * Hkv * t_cap, "own", dev)
+    _need(lens, "lens", torch.int32, B, dev)
+    _need(weights, "weights", torch.float32, B * Hkv * t_cap, dev)
+    need = tq_attend_weigh_scratch_bytes(p, q.dtype, B, Hq, Hkv, Nq, t_cap)
+    if out is None:
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    if scratch is None:
+        scratch = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+    _need_rest(p, q, out, scratch, need, dev_status)
+    _check(_lib.tq_attend_weigh(p.ref, _ptr(q), dt, B, Hq, Hkv, Nq, _ptr(lens), t_cap,
+                                *[_ptr(t) for t in (*keys, *values)], float(scale), _ptr(weights), _ptr(out),
+                                _ptr(scratch), scratch.numel() * scratch.element_size(), _ptr(dev_status), _stream()),
+           "tq_attend_weigh")
+    return out
+
+
+def tq_evict_scratch_bytes(p: Params, B, Hkv, t_cap, budget) -> int:
+    return _lib.tq_evict_scratch_bytes(p.ref, B, Hkv, t_cap, budget)
+
+
+def tq_evict(p: Params, keys, values, weights: torch.Tensor, lens: torch.Tensor, Hkv: int, t_cap: int, budget: int,
+             recent: int, out_cap: int, out_keys=None, out_values=None, out_weights=None, kept=None, out_lens=None,
+             scratch=None, dev_status=None):
+    """Copy each slice's `budget` heaviest tokens by weights (float32 [B, Hkv, t_cap]), the last
+    `recent` ones always among them, in their order into a cache of capacity out_cap.  Returns
+    (out_keys, out_values, out_weights, kept, out_lens): the destination cache, its weights
+    [B, Hkv, out_cap], the kept slots int32 [B, Hkv, budget] and the new lengths int32 [B].
+    Entries behind a slice's kept tokens are not written."""
+    B, dev = lens.numel(), lens.device
+    _on_current(p, dev)
+    n, m = B * Hkv * t_cap, B * Hkv * out_cap
+    _need_cache(p, keys, values, n, "own", dev)
+    _need(lens, "lens", torch.int32, B, dev)
+    _need(weights, "weights", torch.float32, n, dev)
+    new = lambda *shape, dtype: torch.empty(shape, dtype=dtype, device=dev)  # noqa: E731
+    if out_keys is None:
+        out_keys = (new(m, p.key_words(), dtype=torch.int32), new(m, p.proj_dim // 32, dtype=torch.int32),
+                    new(m, dtype=torch.float16), new(m, dtype=torch.float16))
+    if out_values is None:
+        out_values = (new(m, p.value_words(), dtype=torch.int32), new(m, dtype=torch.float16))
+    if out_weights is None:
+        out_weights = new(B, Hkv, out_cap, dtype=torch.float32)
+    if kept is None:
+        kept = new(B, Hkv, budget, dtype=torch.int32)
+    if out_lens is None:
+        out_lens = new(B, dtype=torch.int32)
+    _need_cache(p, out_keys, out_values, m, "destination", dev)
+    _need(out_weights, "out_weights", torch.float32, m, dev)
+    _need(kept, "kept", torch.int32, B * Hkv * budget, dev)
+    _need(out_lens, "out_lens", torch.int32, B, dev)
+    need = tq_evict_scratch_bytes(p, B, Hkv, t_cap, budget)
+    if scratch is None:
+        scratch = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+    if scratch.device != dev or scratch.numel() * scratch.element_size() < need:
+        raise ValueError(f"scratch must hold {need} bytes on {dev}")
+    if dev_status is not None:
+        _need(dev_status, "dev_status", torch.int32, 1, dev)
+    _check(_lib.tq_evict(p.ref, B, Hkv, _ptr(lens), t_cap, *[_ptr(t) for t in (*keys, *values)], _ptr(weights), budget,
+                         recent, out_cap, *[_ptr(t) for t in (*out_keys, *out_values)], _ptr(out_weights), _ptr(kept),
+                         _ptr(out_lens), _ptr(scratch), scratch.numel() * scratch.element_size(), _ptr(dev_status),
+                         _stream()), "tq_evict")
+    return out_keys, out_values, out_weights, kept, out_lens
