@@ -1,0 +1,593 @@
+// tq_ragged_mma.cuh -- attention over caches of different lengths for a few query rows per slice,
+// on the tensor cores (mma.sync m16n8k16), straight from the packed records.
+//
+// A warp takes 32 tokens at a time.  Scores: A = 16 tokens x 16 coordinates decoded from the packed
+// words, B = query rows.  Value sums, transposed: A = 16 coordinates x 16 tokens, B = the softmax
+// weights of the rows.  Both products sum over an index whose order is free (coordinates, tokens),
+// and the rows of the value product may be any permutation of the coordinates, so each lane is
+// given the coordinates that make its decoding cheapest: all of them from one or two words.
+//
+// Decoding.  Codes are turned to fp16 by byte permutation: a register whose nibbles are codes is
+// the selector that picks the high, then the low bytes of four table entries (two permutations a
+// four codes each), and two more interleave them to fp16 pairs.  With K bits a code that is
+// about 1.5 to 2 instructions a value, against 6 and more for shifting each code out; the selectors
+// come from the bit planes by masks (four coordinates a nibble apart, or two tokens interleaved for
+// the value product, whose pairs run along the tokens).  4-bit value codes use the codebook's
+// antisymmetry: a table of 8 magnitudes, the top bit as the sign.
+//
+// Precision.  A query row is split in two fp16 numbers, hi + lo, in two columns of B, whose sums are
+// added: the scores keep 22 bits of Q, and the key operands are exact to 2^-21 (serve_prep_kernel:
+// a well chosen scale for 2 bits, a second table for 3 bits).  Value sums: fp16 weights and
+// centroids for 16-bit outputs; F32 splits both.
+#pragma once
+
+#include <float.h>
+
+#include "tq_serve.cuh"
+
+namespace tq {
+namespace ragged {
+
+constexpr int NW = 4;  // warps per CTA
+
+template <int D, int KB_, int NT_, bool F32_>
+struct Cfg {
+    static constexpr int KB = KB_, VB = KB_ + 1, NT = NT_;
+    static constexpr bool F32 = F32_;
+    static constexpr int ROWS = 4 * NT;  // query rows of a CTA
+    static constexpr int G32 = D / 32, M = D / 2, SW = M / 32;
+    static constexpr int KWPT = KB * G32, VWPT = VB * G32;
+    static constexpr int NG = D >= 128 ? D / 128 : 1;  // key words (of each plane) of a lane
+    static constexpr int NI = D >= 128 ? 4 : 2;        // selectors from one word
+    static constexpr int KC = D / 16, KS = KC + D / 32;  // products: codes, then signs
+    static constexpr int PW = D / 16;                  // sign pairs of a lane
+    static constexpr int LPW = 256 / D;                // lanes that share a sign word
+    static constexpr int VH = D >= 256 ? 2 : 1;        // halves of a value word that a lane takes
+    static constexpr int NO = F32 ? NT : 1;            // value accumulators
+    static constexpr int TILES = D / 16;
+    static constexpr bool BREG = D * NT <= 128;        // query fragments in registers
+    // a stage of the ring: key codes, signs, value codes
+    static constexpr uint32_t OS = kStage * KWPT * 4, OV = OS + kStage * SW * 4, STAGE = OV + kStage * VWPT * 4;
+    static constexpr uint32_t CAP = D >= 256 ? 68 * 1024 : 48 * 1024;
+    static constexpr int NST0 = CAP / (NW * STAGE);
+    static constexpr int NST = NST0 < 2 ? 2 : NST0 > 4 ? 4 : NST0;
+    static constexpr uint32_t MERGE = NW * ROWS * (D + 2) * 4;
+    static constexpr uint32_t RING0 = NW * NST * STAGE, RING = RING0 > MERGE ? RING0 : (MERGE + 15) / 16 * 16;
+    static constexpr uint32_t OMETA = RING, OB = OMETA + NW * 32 * 16, SMEM = OB + NT * KS * 32 * 8;
+};
+
+__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint2 b) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b.x), "r"(b.y));
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
+    uint32_t d;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+    return d;
+}
+
+template <int BYTES>
+__device__ __forceinline__ void cp_async(void *dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src),
+                 "n"(BYTES)
+                 : "memory");
+}
+
+// `words` words that start at a record, in the widest pieces that every record of W words allows.
+template <int W>
+__device__ __forceinline__ void copy_words(void *dst, const uint32_t *src, int words, int lane) {
+    constexpr int G = W % 4 == 0 ? 4 : W % 2 == 0 ? 2 : 1;
+#pragma unroll
+    for (int c = lane; c < kStage * W / G; c += 32)
+        if (c * G < words) cp_async<4 * G>((uint32_t *)dst + c * G, src + c * G);
+}
+
+// (a & m) | (b & ~m)
+__device__ __forceinline__ uint32_t pick(uint32_t a, uint32_t b, uint32_t m) { return (a & m) | (b & ~m); }
+
+// Selectors of N bits: nibble n of x[i] = bits 4 n + i of the planes w[0 .. N-1].
+template <int N>
+__device__ __forceinline__ void selectors(const uint32_t *w, uint32_t (&x)[4]) {
+    if constexpr (N == 1) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = (w[0] >> i) & 0x11111111u;
+    } else {
+        const uint32_t a = pick(w[0], w[1] << 1, 0x55555555u);  // nibble: w0.0 w1.0 w0.2 w1.2
+        const uint32_t b = pick(w[0] >> 1, w[1], 0x55555555u);  // nibble: w0.1 w1.1 w0.3 w1.3
+        if constexpr (N == 2) {
+            x[0] = a & 0x33333333u;
+            x[1] = b & 0x33333333u;
+            x[2] = (a >> 2) & 0x33333333u;
+            x[3] = (b >> 2) & 0x33333333u;
+        } else {
+            x[0] = pick(a, w[2] << 2, 0x33333333u) & 0x77777777u;
+            x[1] = pick(b, w[2] << 1, 0x33333333u) & 0x77777777u;
+            x[2] = pick(a >> 2, w[2], 0x33333333u) & 0x77777777u;
+            x[3] = pick(b >> 2, w[2] >> 1, 0x33333333u) & 0x77777777u;
+        }
+    }
+}
+
+// A table of up to 8 fp16 numbers, its high and its low bytes.
+struct Lut {
+    uint32_t h0, h1, l0, l1;
+};
+
+template <int N>
+__device__ __forceinline__ Lut load_lut(const uint16_t *t) {
+    Lut u = {0, 0, 0, 0};
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        const uint32_t v = t[k];
+        (k < 4 ? u.h0 : u.h1) |= (v >> 8) << (8 * (k & 3));
+        (k < 4 ? u.l0 : u.l1) |= (v & 255u) << (8 * (k & 3));
+    }
+    return u;
+}
+
+// Bytes of (a, b) by the nibbles of `sel`, each 0..7.
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
+    uint32_t r;
+    asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(sel));
+    return r;
+}
+
+// The four numbers that the low 16 bits of the selector pick, as two pairs.  `flip`: bytes to xor
+// into the high bytes.
+__device__ __forceinline__ void look_up(const Lut &t, uint32_t sel, uint32_t flip, uint32_t &p0, uint32_t &p1) {
+    const uint32_t h = prmt(t.h0, t.h1, sel) ^ flip, l = prmt(t.l0, t.l1, sel);
+    p0 = prmt(l, h, 0x5140);
+    p1 = prmt(l, h, 0x7362);
+}
+
+// The coordinate behind element e (0..3) of lane t4 in code product ks, and in sign product ks.
+template <class C, int D>
+__device__ __forceinline__ int code_coord(int t4, int ks, int e) {
+    if constexpr (C::KB == 1) {  // sign-like: pairs of bits l, l + 16
+        const int pairs = D >= 128 ? 16 : 8, j = 2 * ks + (e >> 1), gg = j / pairs, l = j % pairs;
+        const int g = D >= 128 ? t4 * C::NG + gg : t4 >> 1;
+        return 32 * g + (D >= 128 ? 0 : 8 * (t4 & 1)) + l + 16 * (e & 1);
+    } else {
+        const int h = ks & 1, i = (ks >> 1) % C::NI, gg = (ks >> 1) / C::NI;
+        const int g = D >= 128 ? t4 * C::NG + gg : t4 >> 1;
+        return 32 * g + 4 * (4 * h + e) + i + (D >= 128 ? 0 : 2 * (t4 & 1));
+    }
+}
+template <class C, int D>
+__device__ __forceinline__ int sign_coord(int t4, int ks, int e) {
+    return 32 * (t4 / C::LPW) + (t4 % C::LPW) * C::PW + 2 * ks + (e >> 1) + 16 * (e & 1);
+}
+
+// One CTA: its pieces of the slices (tq_serve.cuh) for query rows [ROWS blockIdx.y, ...).  Each warp
+// takes every NW-th stage of a piece through its own ring of asynchronous copies and keeps its own
+// reference, sums and accumulators; they meet at the end of the piece.
+//
+// The reference N of a row moves only when some y exceeds it by more than 8: then the accumulators
+// are rescaled (rare after the first stages), so that the usual path has no reduction over lanes.
+template <int D, int KB, int NT, bool F32>
+__global__ void __launch_bounds__(NW * 32, D >= 256 ? 3 : F32 || NT > 1 ? 3 : 4) ragged_mma_kernel(RaggedArgs a) {
+    using C = Cfg<D, KB, NT, F32>;
+    constexpr int VB = C::VB, VN = VB < 3 ? VB : 3;
+    extern __shared__ __align__(16) uint8_t smem[];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gid = lane >> 2, t4 = lane & 3;
+    const int n = D + C::M;
+    const int64_t total = ragged_total(a.c);
+    const int64_t w1 = cta_first(total, a.c.ctas, blockIdx.x + 1);
+    int64_t w = cta_first(total, a.c.ctas, blockIdx.x);
+    if (w >= w1) return;
+    const int r0 = blockIdx.y * C::ROWS, nr = min(C::ROWS, a.c.rows - r0);
+    const ServeTables *T = a.tables;
+    const Lut kh = load_lut<(1 << KB)>(T->kh);
+    const Lut kl = load_lut<KB == 3 ? 8 : 1>(T->kl);
+    // 4-bit values: the upper half of the table, magnitudes in ascending order
+    const Lut vh = load_lut<(1 << VN)>(T->vh + (VB == 4 ? 8 : 0));
+    const Lut vl = load_lut<F32 ? (1 << VN) : 1>(T->vl + (VB == 4 ? 8 : 0));
+    const float tau = T->tau;
+    uint8_t *ring = smem + (size_t)warp * C::NST * C::STAGE;
+    float4 *meta = (float4 *)(smem + C::OMETA) + warp * 32;
+    uint2 *bfrag = (uint2 *)(smem + C::OB);
+    float *mrg = (float *)smem;
+    const int vg = D >= 256 ? gid : D == 128 ? gid >> 1 : gid >> 2;  // value word of this lane
+    const int vhalf = D >= 256 ? 0 : D == 128 ? gid & 1 : (gid >> 1) & 1;
+
+    Piece pc;
+    for (; w < w1; w += pc.s1 - pc.s0) {
+        pc = piece_at(a.c, w, w1);
+        __syncthreads();  // the last piece's merge is read
+        // ---- query fragments of the slice
+        for (int e = tid; e < NT * C::KS * 32; e += NW * 32) {
+            const int ln = e & 31, ks = (e >> 5) % C::KS, nt = (e >> 5) / C::KS;
+            const int row = 4 * nt + (ln >> 3), part = (ln >> 2) & 1;
+            uint32_t b[2] = {0, 0};
+            if (row < nr) {
+                const float *q = a.qprep + ragged_row(a.c, pc.slice, r0 + row) * n;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float x = ks < C::KC ? q[code_coord<C, D>(ln & 3, ks, k)]
+                                               : q[D + sign_coord<C, D>(ln & 3, ks - C::KC, k)];
+                    const __half hi = __float2half_rn(x);
+                    const __half v = part ? __float2half_rn(x - __half2float(hi)) : hi;
+                    b[k >> 1] |= (uint32_t)__half_as_ushort(v) << (16 * (k & 1));
+                }
+            }
+            bfrag[e] = make_uint2(b[0], b[1]);
+        }
+        float f[NT], N[NT], l[NT], o[C::NO][C::TILES][4];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            const int row = 4 * t + t4;
+            f[t] = row < nr ? a.fscale[ragged_row(a.c, pc.slice, r0 + row)] : 0.f;
+            N[t] = -FLT_MAX;
+            l[t] = 0.f;
+        }
+#pragma unroll
+        for (int t = 0; t < C::NO; ++t)
+#pragma unroll
+            for (int i = 0; i < C::TILES; ++i)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) o[t][i][k] = 0.f;
+        __syncthreads();
+        uint2 breg[C::BREG ? NT * C::KS : 1];
+        if constexpr (C::BREG) {
+#pragma unroll
+            for (int k = 0; k < NT * C::KS; ++k) breg[k] = bfrag[k * 32 + lane];
+        }
+
+        // ---- the warp's stages: pc.s0 + warp, + NW, ...
+        const int64_t rec0 = pc.slice * a.c.stride;
+        auto issue = [&](int64_t s) {
+            if (s < pc.s1) {
+                const int t0 = (int)(s * kStage), nt = min(kStage, pc.len - t0);
+                uint8_t *st = ring + (int)((s - pc.s0) / NW % C::NST) * C::STAGE;
+                const int64_t rec = rec0 + t0;
+                copy_words<C::KWPT>(st, a.c.kcodes + rec * C::KWPT, nt * C::KWPT, lane);
+                copy_words<C::SW>(st + C::OS, a.c.ksigns + rec * C::SW, nt * C::SW, lane);
+                copy_words<C::VWPT>(st + C::OV, a.c.vcodes + rec * C::VWPT, nt * C::VWPT, lane);
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+        uint16_t nk = 0, nrho = 0, nv = 0;  // the next stage's norms, a token a lane
+        auto norms = [&](int64_t s) {
+            const int64_t t = s * kStage + lane;
+            if (s < pc.s1 && t < pc.len) {
+                nk = a.c.knorm[rec0 + t];
+                nrho = a.c.krnorm[rec0 + t];
+                nv = a.c.vnorm[rec0 + t];
+            }
+        };
+        const int64_t first = pc.s0 + warp;
+#pragma unroll
+        for (int k = 0; k < C::NST - 1; ++k) issue(first + k * NW);
+        norms(first);
+        for (int64_t s = first; s < pc.s1; s += NW) {
+            __syncwarp();  // every lane has read the stage whose slot is filled next, and its norms
+            issue(s + (C::NST - 1) * NW);
+            const int t0 = (int)(s * kStage);
+            {
+                // kn, (-rho, -rho), log2 ||v||, 1 / ||v|| (negative where ||v|| is 0); tokens past the
+                // end get y = -inf
+                const bool there = t0 + lane < pc.len;
+                const float v = f16_bits_to_f32(nv), vc = fmaxf(v, kMinNorm);
+                float4 x;
+                x.x = there ? f16_bits_to_f32(nk) : 0.f;
+                const uint32_t neg = there ? (uint32_t)(nrho ^ 0x8000u) : 0u;
+                x.y = __uint_as_float(neg | (neg << 16));
+                x.z = !there ? -INFINITY : v != v ? v : log2f(vc);
+                x.w = v == 0.f ? -1.f / vc : 1.f / vc;
+                meta[lane] = x;
+            }
+            norms(s + NW);
+            asm volatile("cp.async.wait_group %0;" ::"n"(C::NST - 1) : "memory");
+            __syncwarp();
+            const uint8_t *st = ring + (int)((s - pc.s0) / NW % C::NST) * C::STAGE;
+            const uint32_t *skc = (const uint32_t *)st, *sks = (const uint32_t *)(st + C::OS),
+                           *svc = (const uint32_t *)(st + C::OV);
+            auto bf = [&](int nt, int ks) -> uint2 {
+                if constexpr (C::BREG) return breg[nt * C::KS + ks];
+                else return bfrag[(nt * C::KS + ks) * 32 + lane];
+            };
+#pragma unroll
+            for (int blk = 0; blk < 2; ++blk) {
+                // ---- scores of 16 tokens: this lane's are tA and tA + 8, of rows 4 nt + t4
+                const int tA = 16 * blk + gid;
+                const float4 mA = meta[tA], mB = meta[tA + 8];
+                float acc[NT][4];
+#pragma unroll
+                for (int t = 0; t < NT; ++t) acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = 0.f;
+#pragma unroll
+                for (int gg = 0; gg < C::NG; ++gg) {
+                    const int g = D >= 128 ? t4 * C::NG + gg : t4 >> 1;
+                    uint32_t wA[KB], wB[KB];
+#pragma unroll
+                    for (int p = 0; p < KB; ++p) {
+                        wA[p] = skc[tA * C::KWPT + g * KB + p];
+                        wB[p] = skc[(tA + 8) * C::KWPT + g * KB + p];
+                    }
+                    if constexpr (KB == 1) {
+                        constexpr int PR = D >= 128 ? 16 : 8;
+                        if (D < 128) {
+                            wA[0] <<= 8 * (1 - (t4 & 1));
+                            wB[0] <<= 8 * (1 - (t4 & 1));
+                        }
+                        constexpr uint32_t one = 0xBC00BC00u;  // (-1, -1)
+#pragma unroll
+                        for (int k = 0; k < PR / 2; ++k) {
+                            const uint32_t a0 = ((wA[0] << (PR - 1 - 2 * k)) & 0x80008000u) ^ one;
+                            const uint32_t a1 = ((wB[0] << (PR - 1 - 2 * k)) & 0x80008000u) ^ one;
+                            const uint32_t a2 = ((wA[0] << (PR - 2 - 2 * k)) & 0x80008000u) ^ one;
+                            const uint32_t a3 = ((wB[0] << (PR - 2 - 2 * k)) & 0x80008000u) ^ one;
+#pragma unroll
+                            for (int t = 0; t < NT; ++t) mma(acc[t], a0, a1, a2, a3, bf(t, gg * (PR / 2) + k));
+                        }
+                    } else {
+                        if (D < 128) {
+#pragma unroll
+                            for (int p = 0; p < KB; ++p) {
+                                wA[p] >>= 2 * (t4 & 1);
+                                wB[p] >>= 2 * (t4 & 1);
+                            }
+                        }
+                        uint32_t xA[4], xB[4];
+                        selectors<KB>(wA, xA);
+                        selectors<KB>(wB, xB);
+#pragma unroll
+                        for (int i = 0; i < C::NI; ++i)
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                const int ks = (gg * C::NI + i) * 2 + h;
+                                uint32_t a0, a1, a2, a3;
+                                look_up(kh, xA[i] >> (16 * h), 0u, a0, a2);
+                                look_up(kh, xB[i] >> (16 * h), 0u, a1, a3);
+#pragma unroll
+                                for (int t = 0; t < NT; ++t) mma(acc[t], a0, a1, a2, a3, bf(t, ks));
+                                if constexpr (KB == 3) {
+                                    look_up(kl, xA[i] >> (16 * h), 0u, a0, a2);
+                                    look_up(kl, xB[i] >> (16 * h), 0u, a1, a3);
+#pragma unroll
+                                    for (int t = 0; t < NT; ++t) mma(acc[t], a0, a1, a2, a3, bf(t, ks));
+                                }
+                            }
+                    }
+                }
+                {
+                    const int sh = 16 - C::PW - (t4 % C::LPW) * C::PW;
+                    const uint32_t sA = sks[tA * C::SW + t4 / C::LPW] << sh;
+                    const uint32_t sB = sks[(tA + 8) * C::SW + t4 / C::LPW] << sh;
+                    const uint32_t nA = __float_as_uint(mA.y), nB = __float_as_uint(mB.y);
+#pragma unroll
+                    for (int k = 0; k < C::PW / 2; ++k) {
+                        const uint32_t a0 = ((sA << (C::PW - 1 - 2 * k)) & 0x80008000u) ^ nA;
+                        const uint32_t a1 = ((sB << (C::PW - 1 - 2 * k)) & 0x80008000u) ^ nB;
+                        const uint32_t a2 = ((sA << (C::PW - 2 - 2 * k)) & 0x80008000u) ^ nA;
+                        const uint32_t a3 = ((sB << (C::PW - 2 - 2 * k)) & 0x80008000u) ^ nB;
+#pragma unroll
+                        for (int t = 0; t < NT; ++t) mma(acc[t], a0, a1, a2, a3, bf(t, C::KC + k));
+                    }
+                }
+                // ---- weights
+                float yA[NT], yB[NT];
+                bool over = false;
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    const float zA = (acc[t][0] + acc[t][1]) * (mA.x * f[t]);
+                    const float zB = (acc[t][2] + acc[t][3]) * (mB.x * f[t]);
+                    if (a.zbuf && 4 * t + t4 < nr) {
+                        float *zp = a.zbuf + ((int64_t)pc.slice * a.c.rows + r0 + 4 * t + t4) * a.c.stride + t0 + tA;
+                        if (t0 + tA < pc.len) zp[0] = zA;
+                        if (t0 + tA + 8 < pc.len) zp[8] = zB;
+                    }
+                    yA[t] = zA + mA.z;
+                    yB[t] = zB + mB.z;
+                    over |= fmaxf(yA[t], yB[t]) > N[t] + 8.f;
+                }
+                if (__any_sync(kFull, over)) {
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) {
+                        float mx = fmaxf(yA[t], yB[t]);
+                        mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 4));
+                        mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 8));
+                        mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 16));
+                        mx = fmaxf(mx, N[t]);
+                        const float sc = exp2f(N[t] - mx);
+                        N[t] = mx;
+                        l[t] *= sc;
+#pragma unroll
+                        for (int i = 0; i < C::TILES; ++i) {
+                            if constexpr (F32 || NT == 1) {
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) o[F32 ? t : 0][i][k] *= sc;
+                            } else {
+                                o[0][i][t] *= sc;
+                                o[0][i][2 + t] *= sc;
+                            }
+                        }
+                    }
+                }
+                // B of the value product: column 2 t4 + c of this lane is (row t4; hi, lo) when F32 or
+                // with one row tile (lo = 0 then), and row 4 c + t4 with two
+                uint2 pb[C::NO];
+                {
+                    float pA[NT], pB[NT];
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) {
+                        pA[t] = exp2f(yA[t] - N[t]);
+                        pB[t] = exp2f(yB[t] - N[t]);
+                        l[t] = fmaf(pA[t], fabsf(mA.w), l[t]);
+                        l[t] = fmaf(pB[t], fabsf(mB.w), l[t]);
+                        pA[t] = mA.w < 0.f ? 0.f : pA[t];
+                        pB[t] = mB.w < 0.f ? 0.f : pB[t];
+                    }
+#pragma unroll
+                    for (int t = 0; t < C::NO; ++t) {
+                        __half2 hA, hB;
+                        if constexpr (F32) {
+                            const __half uA = __float2half_rn(pA[t]), uB = __float2half_rn(pB[t]);
+                            hA = __halves2half2(uA, __float2half_rn(pA[t] - __half2float(uA)));
+                            hB = __halves2half2(uB, __float2half_rn(pB[t] - __half2float(uB)));
+                        } else {
+                            hA = __floats2half2_rn(pA[0], NT > 1 ? pA[NT - 1] : 0.f);
+                            hB = __floats2half2_rn(pB[0], NT > 1 ? pB[NT - 1] : 0.f);
+                        }
+                        pb[t].x = transpose8x8(*(uint32_t *)&hA);
+                        pb[t].y = transpose8x8(*(uint32_t *)&hB);
+                    }
+                }
+                // ---- value sums: tokens 2 t4, 2 t4 + 1 (AB) and 8 + 2 t4, 9 + 2 t4 (CD) of the block
+                const int tV = 16 * blk + 2 * t4;
+                uint32_t wv[4][VB];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+#pragma unroll
+                    for (int p = 0; p < VB; ++p)
+                        wv[k][p] = svc[(tV + (k & 1) + 8 * (k >> 1)) * C::VWPT + vg * VB + p];
+                if constexpr (VB == 4) {  // magnitude selectors: the code's low bits, inverted below the middle
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+#pragma unroll
+                        for (int p = 0; p < 3; ++p) wv[k][p] = ~(wv[k][p] ^ wv[k][3]);
+                }
+#pragma unroll
+                for (int hv = 0; hv < C::VH; ++hv) {
+                    // two tokens a byte: four bits of each, of one half of every byte of the words
+                    uint32_t y[2][VB];
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+#pragma unroll
+                        for (int p = 0; p < VB; ++p) {
+                            const int hs = D >= 256 ? hv : vhalf;
+                            y[k][p] = pick(wv[2 * k][p] >> (4 * hs), wv[2 * k + 1][p] << (4 - 4 * hs), 0x0F0F0F0Fu);
+                            if (D < 128) y[k][p] >>= 2 * (gid & 1);
+                        }
+                    uint32_t x[2][4];
+                    selectors<VN>(y[0], x[0]);
+                    selectors<VN>(y[1], x[1]);
+#pragma unroll
+                    for (int i = 0; i < C::NI; ++i) {
+                        uint32_t sg[2] = {0, 0};
+                        if constexpr (VB == 4) {
+                            sg[0] = (y[0][3] >> i) & 0x11111111u;
+                            sg[1] = (y[1][3] >> i) & 0x11111111u;
+                        }
+#pragma unroll
+                        for (int kk = 0; kk < 2; ++kk) {
+                            const int tile = (hv * C::NI + i) * 2 + kk;
+                            const uint32_t f0 = VB == 4 ? prmt(0x80u, 0u, sg[0] >> (16 * kk)) : 0u;
+                            const uint32_t f1 = VB == 4 ? prmt(0x80u, 0u, sg[1] >> (16 * kk)) : 0u;
+                            uint32_t a0, a1, a2, a3;
+                            look_up(vh, x[0][i] >> (16 * kk), f0, a0, a1);
+                            look_up(vh, x[1][i] >> (16 * kk), f1, a2, a3);
+#pragma unroll
+                            for (int t = 0; t < C::NO; ++t) mma(o[t][tile], a0, a1, a2, a3, pb[t]);
+                            if constexpr (F32) {
+                                look_up(vl, x[0][i] >> (16 * kk), f0, a0, a1);
+                                look_up(vl, x[1][i] >> (16 * kk), f1, a2, a3);
+#pragma unroll
+                                for (int t = 0; t < C::NO; ++t) mma(o[t][tile], a0, a1, a2, a3, pb[t]);
+                            }
+                        }
+                    }
+                }
+            }
+        }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        __syncthreads();  // every warp is done with its ring
+
+        // ---- the warps' results meet: [warp][row](N, l), then [warp][row][d]
+        float *mo = mrg + NW * C::ROWS * 2;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            float s = l[t];
+            s += __shfl_xor_sync(kFull, s, 4);
+            s += __shfl_xor_sync(kFull, s, 8);
+            s += __shfl_xor_sync(kFull, s, 16);
+            if (gid == 0) {
+                mrg[(warp * C::ROWS + 4 * t + t4) * 2] = N[t];
+                mrg[(warp * C::ROWS + 4 * t + t4) * 2 + 1] = s;
+            }
+        }
+#pragma unroll
+        for (int hv = 0; hv < C::VH; ++hv)
+#pragma unroll
+            for (int i = 0; i < C::NI; ++i)
+#pragma unroll
+                for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+                    for (int up = 0; up < 2; ++up) {
+                        const int tile = (hv * C::NI + i) * 2 + kk;
+                        const int j = 32 * vg + 16 * kk + 8 * up + 4 * (D >= 256 ? hv : vhalf) + i +
+                                      (D >= 128 ? 0 : 2 * (gid & 1));
+                        float *at = mo + (size_t)warp * C::ROWS * D + j;
+                        if constexpr (F32 || NT == 1) {
+#pragma unroll
+                            for (int t = 0; t < C::NO; ++t)
+                                at[(4 * t + t4) * D] = o[t][tile][2 * up] + o[t][tile][2 * up + 1];
+                        } else {
+                            at[t4 * D] = o[0][tile][2 * up];
+                            at[(4 + t4) * D] = o[0][tile][2 * up + 1];
+                        }
+                    }
+        __syncthreads();
+        for (int e = tid; e < nr * D; e += NW * 32) {
+            const int r = e / D, j = e % D;
+            float Nm = -FLT_MAX;
+#pragma unroll
+            for (int u = 0; u < NW; ++u) Nm = fmaxf(Nm, mrg[(u * C::ROWS + r) * 2]);
+            float s = 0.f, L = 0.f;
+#pragma unroll
+            for (int u = 0; u < NW; ++u) {
+                const float sc = exp2f(mrg[(u * C::ROWS + r) * 2] - Nm);
+                s = fmaf(sc, mo[((size_t)u * C::ROWS + r) * D + j], s);
+                L = fmaf(sc, mrg[(u * C::ROWS + r) * 2 + 1], L);
+            }
+            float *pp = a.part + ((int64_t)(blockIdx.x + pc.slice) * a.c.rows + r0 + r) * partial_stride(D);
+            pp[4 + j] = s * tau;
+            if (j == 0) {
+                pp[0] = Nm;
+                pp[1] = L;
+            }
+        }
+    }
+}
+
+template <int D, int KB, int NT, bool F32>
+cudaError_t launch_one(const RaggedArgs &a, cudaStream_t s) {
+    using C = Cfg<D, KB, NT, F32>;
+    cudaError_t e = cudaFuncSetAttribute(ragged_mma_kernel<D, KB, NT, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)C::SMEM);
+    if (e != cudaSuccess) return e;
+    dim3 grid((unsigned)a.c.ctas, (unsigned)((a.c.rows + C::ROWS - 1) / C::ROWS));
+    ragged_mma_kernel<D, KB, NT, F32><<<grid, NW * 32, C::SMEM, s>>>(a);
+    return cudaGetLastError();
+}
+
+// The instances of one head dimension; defined in tq_ragged_<D>.cu.
+template <int D>
+cudaError_t launch_dim(const RaggedArgs &a, bool f32, int row_block, cudaStream_t s);
+
+template <int D, int KB>
+cudaError_t launch_bits(const RaggedArgs &a, bool f32, int row_block, cudaStream_t s) {
+    if (f32) {
+        if constexpr (D < 256) {
+            if (row_block == 8) return launch_one<D, KB, 2, true>(a, s);
+        }
+        return launch_one<D, KB, 1, true>(a, s);
+    }
+    return row_block == 8 ? launch_one<D, KB, 2, false>(a, s) : launch_one<D, KB, 1, false>(a, s);
+}
+
+#define TQ_RAGGED_DIM(D)                                                                              \
+    template <>                                                                                       \
+    cudaError_t launch_dim<D>(const RaggedArgs &a, bool f32, int row_block, cudaStream_t s) {         \
+        switch (a.P.kbeta) {                                                                          \
+            case 1: return launch_bits<D, 1>(a, f32, row_block, s);                                   \
+            case 2: return launch_bits<D, 2>(a, f32, row_block, s);                                   \
+            case 3: return launch_bits<D, 3>(a, f32, row_block, s);                                   \
+            default: return cudaErrorInvalidValue;                                                    \
+        }                                                                                             \
+    }
+
+}  // namespace ragged
+}  // namespace tq

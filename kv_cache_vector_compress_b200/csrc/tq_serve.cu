@@ -423,7 +423,7 @@ __global__ void __launch_bounds__(kMgThreads) serve_merge_kernel(MergeArgs a) {
                 }
             L = warp_sum(L);
             inv = L != 0.f ? 1.f / L : 0.f;
-            if (lane == 0 && a.lse) a.lse[row] = N == -INFINITY ? INFINITY : N + log2f(L);
+            if (lane == 0 && a.lse) a.lse[row] = L == 0.f ? INFINITY : N + log2f(L);
         }
         for (int j0 = 0; j0 < d; j0 += 32) {
             const int j = j0 + lane;
@@ -489,6 +489,36 @@ cudaError_t launch_ragged_plain(const RaggedArgs &a, cudaStream_t s) {
     return cudaGetLastError();
 }
 
+namespace ragged {
+template <int D>
+cudaError_t launch_dim(const RaggedArgs &a, bool f32, int row_block, cudaStream_t s);
+extern template cudaError_t launch_dim<64>(const RaggedArgs &, bool, int, cudaStream_t);
+extern template cudaError_t launch_dim<128>(const RaggedArgs &, bool, int, cudaStream_t);
+extern template cudaError_t launch_dim<256>(const RaggedArgs &, bool, int, cudaStream_t);
+}  // namespace ragged
+
+bool ragged_mma_supported(const Prepared &P) {
+    return (P.d == 64 || P.d == 128 || P.d == 256) && P.m == P.d / 2 && P.kbeta >= 1 && P.kbeta <= 3 &&
+           P.vbeta == P.kbeta + 1;
+}
+
+// Eight rows a CTA when there are more than four, but for 32-bit results of 256 coordinates, whose
+// accumulators would not fit the registers.
+int ragged_mma_rows(const Prepared &P, bool f32, int64_t rows) {
+    return rows <= 4 || (f32 && P.d >= 256) ? 4 : 8;
+}
+
+int ragged_mma_ctas_per_sm(const Prepared &P) { return P.d >= 256 ? 3 : 4; }
+
+cudaError_t launch_ragged_mma(const RaggedArgs &a, bool f32, int row_block, cudaStream_t s) {
+    switch (a.P.d) {
+        case 64: return ragged::launch_dim<64>(a, f32, row_block, s);
+        case 128: return ragged::launch_dim<128>(a, f32, row_block, s);
+        case 256: return ragged::launch_dim<256>(a, f32, row_block, s);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
 namespace {
 // CTAs among which the stages of a cache are divided: enough to fill the GPU once together with
 // the row blocks, and no more than there are stages.
@@ -506,13 +536,18 @@ ServePlan plan_serve(const Prepared &P, tq_dtype dtype, int B, int Hq, int Hkv, 
     memset(&p, 0, sizeof(p));
     const int R = Hq / Hkv * Nq;
     const int64_t rows = (int64_t)B * Hq * Nq, n = P.d + P.m;
-    (void)dtype;
-    p.fast = false;
+    const bool f32 = dtype == TQ_F32;
+    p.fast = ragged_mma_supported(P);
     p.row_block = kPlRows;
-    const int per_sm = 4;
+    p.prefix_block = kPlRows;
+    const int per_sm = p.fast ? ragged_mma_ctas_per_sm(P) : 4;
+    if (p.fast) {
+        p.row_block = ragged_mma_rows(P, f32, R);
+        p.prefix_block = ragged_mma_rows(P, f32, (int64_t)B * R);
+    }
     if (t_cap > 0) p.own_ctas = division((int64_t)B * Hkv, t_cap, (R + p.row_block - 1) / p.row_block, per_sm);
     if (t_prefix > 0)
-        p.prefix_ctas = division(Hkv, t_prefix, ((int64_t)B * R + p.row_block - 1) / p.row_block, per_sm);
+        p.prefix_ctas = division(Hkv, t_prefix, ((int64_t)B * R + p.prefix_block - 1) / p.prefix_block, per_sm);
     size_t o = 0;
     auto take = [&](size_t bytes) {
         const size_t at = o;
@@ -577,7 +612,7 @@ cudaError_t launch_serve(const ServeCall &call, const ServePlan &plan, void *scr
         own.c.ctas = plan.own_ctas;
         own.part = (float *)(base + plan.own_part);
         own.zbuf = call.weights ? (float *)(base + plan.zbuf) : nullptr;
-        e = launch_ragged_plain(own, s);
+        e = plan.fast ? launch_ragged_mma(own, call.dtype == TQ_F32, plan.row_block, s) : launch_ragged_plain(own, s);
         if (e != cudaSuccess) return e;
     }
     if (plan.prefix_ctas) {
@@ -591,7 +626,8 @@ cudaError_t launch_serve(const ServeCall &call, const ServePlan &plan, void *scr
         pre.c.rows_outer = (int64_t)call.Hkv * R;
         pre.c.ctas = plan.prefix_ctas;
         pre.part = (float *)(base + plan.pre_part);
-        e = launch_ragged_plain(pre, s);
+        e = plan.fast ? launch_ragged_mma(pre, call.dtype == TQ_F32, plan.prefix_block, s)
+                      : launch_ragged_plain(pre, s);
         if (e != cudaSuccess) return e;
     }
     MergeArgs ma;

@@ -124,7 +124,8 @@ struct ServeCall {
 // How a call is computed: by sizes alone, so that the scratch size follows from them too.
 struct ServePlan {
     bool fast;         // the tensor-core kernels (else the plain kernel)
-    int row_block;     // query rows a CTA of the ragged kernel takes
+    int row_block;     // query rows a CTA of the ragged kernel takes, own caches
+    int prefix_block;  // ... and the prefix
     int own_ctas;      // division of the own caches (0: no own caches)
     int prefix_ctas;   // division of the prefix by the ragged kernel (0: not by it)
     // byte offsets in the scratch
@@ -147,7 +148,7 @@ struct RaggedArgs {
 };
 cudaError_t launch_ragged_plain(const RaggedArgs &a, cudaStream_t s);
 bool ragged_mma_supported(const Prepared &P);
-int ragged_mma_rows(const Prepared &P, bool f32, int rows);  // the row block for so many rows a slice
+int ragged_mma_rows(const Prepared &P, bool f32, int64_t rows);  // the row block for so many rows a slice
 int ragged_mma_ctas_per_sm(const Prepared &P);
 cudaError_t launch_ragged_mma(const RaggedArgs &a, bool f32, int row_block, cudaStream_t s);
 
