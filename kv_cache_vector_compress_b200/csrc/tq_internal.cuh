@@ -24,6 +24,16 @@ struct Codebooks {
     float vc[kMaxLevels];  // value centroids
 };
 
+// 16-bit operand tables of the codebooks (fp16 bits) for the serving kernels, and the scales of the
+// query operands that go with them.
+struct ServeTables {
+    uint16_t kh[8], kl[8];    // c_k / sigma = kh + kl for the keys' codebook
+    uint16_t vh[16], vl[16];  // c_v / tau = vh + vl for the values'
+    float sigma, tau;
+    float qbound;  // max over i of (sigma ||R_i||, sqrt(pi/2)/m ||S_i||): |operand| <= qbound ||q||
+    float pad;
+};
+
 // Byte offsets of the prepared arrays inside the caller's workspace.
 struct WsLayout {
     size_t header;     // WsHeader
@@ -37,6 +47,7 @@ struct WsLayout {
     size_t RSsw;       // fp16 hi | lo of [R; S] * 2^kRScaleLog2 (d + m rows), same layout
     size_t S;          // fp32 [m, d]      copy of S
     size_t Sp;         // fp32 [m, d]      S R^T
+    size_t serve;      // ServeTables
     size_t total;
 };
 
@@ -87,6 +98,8 @@ inline WsLayout ws_layout(int d, int m) {
     o = align_up(o + sizeof(float) * (size_t)d * (m > 0 ? m : 1), 256);
     L.Sp = o;
     o = align_up(o + sizeof(float) * (size_t)d * (m > 0 ? m : 1), 256);
+    L.serve = o;
+    o = align_up(o + sizeof(ServeTables), 256);
     L.total = o;
     return L;
 }
@@ -97,6 +110,7 @@ struct Prepared {
     const Codebooks *cb;
     const float *R, *RT, *ST, *SpT, *S, *Sp;
     const uint16_t *Rsw, *Ssw, *RSsw;
+    const ServeTables *serve;
 };
 
 inline Prepared prepared_view(const tq_params *p) {
@@ -117,6 +131,7 @@ inline Prepared prepared_view(const tq_params *p) {
     v.RSsw = (const uint16_t *)(w + L.RSsw);
     v.S = (const float *)(w + L.S);
     v.Sp = (const float *)(w + L.Sp);
+    v.serve = (const ServeTables *)(w + L.serve);
     return v;
 }
 

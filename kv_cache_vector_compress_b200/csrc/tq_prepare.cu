@@ -1,4 +1,7 @@
 // tq_prepare.cu -- derive the kernels' operand copies of R and S into the workspace.
+#include <math.h>
+
+#include "tq_common.cuh"
 #include "tq_internal.cuh"
 
 namespace tq {
@@ -78,6 +81,75 @@ __global__ void prepare_kernel(const float *__restrict__ R, const float *__restr
     }
 }
 
+// The workspace's serve tables; qbound from the rows of R and S (one CTA, a warp a row).
+__global__ void __launch_bounds__(1024) prepare_serve_kernel(const float *__restrict__ R, const float *__restrict__ S,
+                                                             int d, int m, ServeTables t,
+                                                             ServeTables *__restrict__ out) {
+    __shared__ float wmax[32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const float gamma = m > 0 ? sqrtf(1.5707963267948966f) / (float)m : 0.f;
+    float best = 0.f;
+    for (int r = warp; r < d + m; r += 32) {
+        const float *row = r < d ? R + (int64_t)r * d : S + (int64_t)(r - d) * d;
+        float s = 0.f;
+        for (int j = lane; j < d; j += 32) s = fmaf(row[j], row[j], s);
+        s = sqrtf(warp_sum(s)) * (r < d ? t.sigma : gamma);
+        best = fmaxf(best, s);
+    }
+    if (lane == 0) wmax[warp] = best;
+    __syncthreads();
+    if (warp == 0) {
+        best = warp_max(wmax[lane]);
+        if (lane == 0) {
+            t.qbound = best;
+            *out = t;
+        }
+    }
+}
+
+void split_f16(double v, uint16_t *hi, uint16_t *lo) {
+    const __half h = __float2half_rn((float)v);
+    *hi = __half_as_ushort(h);
+    *lo = __half_as_ushort(__float2half_rn((float)(v - (double)__half2float(h))));
+}
+
+double off_f16(double v) { return v - (double)__half2float(__float2half_rn((float)v)); }
+
+// A codebook's operand is its centroids over a scale that may be anything, so it is chosen for the
+// centroids to land near fp16 numbers: of 1024 scales that put the largest one on an fp16 number
+// (in [8, 16), so that low halves are normal numbers too), the one with the least squared error by
+// cell mass.  1 bit: exact.  2 bits: one ratio to approximate, about 2^-21 off for the Gaussian law,
+// so that one fp16 operand serves 32-bit scores.  More bits: the error falls by 2 to 4.
+double table_scale(const float *c, const float *b, int K, int dim) {
+    const int h = K / 2;
+    double best = INFINITY, scale = 1.0;
+    for (int i = 0; i < 1024; ++i) {
+        const double s = (double)c[K - 1] / (8.0 * (1.0 + i * (1.0 / 1024.0)));
+        double e = 0.0;
+        for (int k = h; k < K; ++k) {
+            const double lo = k > h ? b[k - 1] : 0.0, up = k < K - 1 ? b[k] : 2.0 * c[k] - lo;
+            const double x = off_f16(c[k] / s) * s;
+            e += x * x * (up - lo) * exp(-0.5 * dim * (double)c[k] * c[k]);
+        }
+        if (e < best) {
+            best = e;
+            scale = s;
+        }
+    }
+    return scale;
+}
+
+ServeTables serve_tables(const Codebooks &cb, int bits, int dim) {
+    ServeTables t = {};
+    const int V = 1 << bits, K = V / 2;
+    const double tau = table_scale(cb.vc, cb.vb, V, dim), sigma = bits > 1 ? table_scale(cb.kc, cb.kb, K, dim) : 1.0;
+    t.tau = (float)tau;
+    t.sigma = (float)sigma;
+    for (int k = 0; k < V; ++k) split_f16(cb.vc[k] / (double)t.tau, &t.vh[k], &t.vl[k]);
+    for (int k = 0; bits > 1 && k < K; ++k) split_f16(cb.kc[k] / (double)t.sigma, &t.kh[k], &t.kl[k]);
+    return t;
+}
+
 }  // namespace
 
 cudaError_t launch_prepare(const tq_params *p, const Codebooks &cb, cudaStream_t s) {
@@ -89,6 +161,10 @@ cudaError_t launch_prepare(const tq_params *p, const Codebooks &cb, cudaStream_t
     if (blocks < 1) blocks = 1;
     prepare_kernel<<<blocks, 256, 0, s>>>(p->R, p->S, p->dim, p->proj_dim, cb, h,
                                          (char *)p->workspace, L);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    prepare_serve_kernel<<<1, 1024, 0, s>>>(p->R, p->S, p->dim, p->proj_dim, serve_tables(cb, p->bits, p->dim),
+                                            (ServeTables *)((char *)p->workspace + L.serve));
     return cudaGetLastError();
 }
 

@@ -16,8 +16,8 @@
 // antisymmetry: a table of 8 magnitudes, the top bit as the sign.
 //
 // Precision.  A query row is split in two fp16 numbers, hi + lo, in two columns of B, whose sums are
-// added: the scores keep 22 bits of Q, and the key operands are exact to 2^-21 (serve_prep_kernel:
-// a well chosen scale for 2 bits, a second table for 3 bits).  Value sums: fp16 weights and
+// added: the scores keep 22 bits of Q, and the key operands are exact to 2^-21 (ServeTables: a
+// well chosen scale for 2 bits, a second table for 3 bits).  Value sums: fp16 weights and
 // centroids for 16-bit outputs; F32 splits both.
 #pragma once
 
@@ -53,7 +53,7 @@ struct Cfg {
     static constexpr int NST = NST0 < 2 ? 2 : NST0 > 4 ? 4 : NST0;
     static constexpr uint32_t MERGE = NW * ROWS * (D + 2) * 4;
     static constexpr uint32_t RING0 = NW * NST * STAGE, RING = RING0 > MERGE ? RING0 : (MERGE + 15) / 16 * 16;
-    static constexpr uint32_t OMETA = RING, OB = OMETA + NW * 32 * 16, SMEM = OB + NT * KS * 32 * 8;
+    static constexpr uint32_t OMETA = RING, OB = OMETA + NW * 32 * 16, SMEM = OB + (BREG ? 0 : NT * KS * 32 * 8);
 };
 
 __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint2 b) {
@@ -143,24 +143,6 @@ __device__ __forceinline__ void look_up(const Lut &t, uint32_t sel, uint32_t fli
     p1 = prmt(l, h, 0x7362);
 }
 
-// The coordinate behind element e (0..3) of lane t4 in code product ks, and in sign product ks.
-template <class C, int D>
-__device__ __forceinline__ int code_coord(int t4, int ks, int e) {
-    if constexpr (C::KB == 1) {  // sign-like: pairs of bits l, l + 16
-        const int pairs = D >= 128 ? 16 : 8, j = 2 * ks + (e >> 1), gg = j / pairs, l = j % pairs;
-        const int g = D >= 128 ? t4 * C::NG + gg : t4 >> 1;
-        return 32 * g + (D >= 128 ? 0 : 8 * (t4 & 1)) + l + 16 * (e & 1);
-    } else {
-        const int h = ks & 1, i = (ks >> 1) % C::NI, gg = (ks >> 1) / C::NI;
-        const int g = D >= 128 ? t4 * C::NG + gg : t4 >> 1;
-        return 32 * g + 4 * (4 * h + e) + i + (D >= 128 ? 0 : 2 * (t4 & 1));
-    }
-}
-template <class C, int D>
-__device__ __forceinline__ int sign_coord(int t4, int ks, int e) {
-    return 32 * (t4 / C::LPW) + (t4 % C::LPW) * C::PW + 2 * ks + (e >> 1) + 16 * (e & 1);
-}
-
 // One CTA: its pieces of the slices (tq_serve.cuh) for query rows [ROWS blockIdx.y, ...).  Each warp
 // takes every NW-th stage of a piece through its own ring of asynchronous copies and keeps its own
 // reference, sums and accumulators; they meet at the end of the piece.
@@ -173,13 +155,12 @@ __global__ void __launch_bounds__(NW * 32, D >= 256 ? 3 : F32 || NT > 1 ? 3 : 4)
     constexpr int VB = C::VB, VN = VB < 3 ? VB : 3;
     extern __shared__ __align__(16) uint8_t smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gid = lane >> 2, t4 = lane & 3;
-    const int n = D + C::M;
     const int64_t total = ragged_total(a.c);
     const int64_t w1 = cta_first(total, a.c.ctas, blockIdx.x + 1);
     int64_t w = cta_first(total, a.c.ctas, blockIdx.x);
     if (w >= w1) return;
     const int r0 = blockIdx.y * C::ROWS, nr = min(C::ROWS, a.c.rows - r0);
-    const ServeTables *T = a.tables;
+    const ServeTables *T = a.P.serve;
     const Lut kh = load_lut<(1 << KB)>(T->kh);
     const Lut kl = load_lut<KB == 3 ? 8 : 1>(T->kl);
     // 4-bit values: the upper half of the table, magnitudes in ascending order
@@ -198,22 +179,13 @@ __global__ void __launch_bounds__(NW * 32, D >= 256 ? 3 : F32 || NT > 1 ? 3 : 4)
         pc = piece_at(a.c, w, w1);
         __syncthreads();  // the last piece's merge is read
         // ---- query fragments of the slice
-        for (int e = tid; e < NT * C::KS * 32; e += NW * 32) {
-            const int ln = e & 31, ks = (e >> 5) % C::KS, nt = (e >> 5) / C::KS;
-            const int row = 4 * nt + (ln >> 3), part = (ln >> 2) & 1;
-            uint32_t b[2] = {0, 0};
-            if (row < nr) {
-                const float *q = a.qprep + ragged_row(a.c, pc.slice, r0 + row) * n;
+        const uint2 *qf = a.frag + ((int64_t)pc.slice * gridDim.y + blockIdx.y) * (NT * C::KS * 32);
+        uint2 breg[C::BREG ? NT * C::KS : 1];
+        if constexpr (C::BREG) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float x = ks < C::KC ? q[code_coord<C, D>(ln & 3, ks, k)]
-                                               : q[D + sign_coord<C, D>(ln & 3, ks - C::KC, k)];
-                    const __half hi = __float2half_rn(x);
-                    const __half v = part ? __float2half_rn(x - __half2float(hi)) : hi;
-                    b[k >> 1] |= (uint32_t)__half_as_ushort(v) << (16 * (k & 1));
-                }
-            }
-            bfrag[e] = make_uint2(b[0], b[1]);
+            for (int k = 0; k < NT * C::KS; ++k) breg[k] = qf[k * 32 + lane];
+        } else {
+            for (int e = tid; e < NT * C::KS * 32; e += NW * 32) bfrag[e] = qf[e];
         }
         float f[NT], N[NT], l[NT], o[C::NO][C::TILES][4];
 #pragma unroll
@@ -229,12 +201,7 @@ __global__ void __launch_bounds__(NW * 32, D >= 256 ? 3 : F32 || NT > 1 ? 3 : 4)
             for (int i = 0; i < C::TILES; ++i)
 #pragma unroll
                 for (int k = 0; k < 4; ++k) o[t][i][k] = 0.f;
-        __syncthreads();
-        uint2 breg[C::BREG ? NT * C::KS : 1];
-        if constexpr (C::BREG) {
-#pragma unroll
-            for (int k = 0; k < NT * C::KS; ++k) breg[k] = bfrag[k * 32 + lane];
-        }
+        if constexpr (!C::BREG) __syncthreads();
 
         // ---- the warp's stages: pc.s0 + warp, + NW, ...
         const int64_t rec0 = pc.slice * a.c.stride;
@@ -312,7 +279,7 @@ __global__ void __launch_bounds__(NW * 32, D >= 256 ? 3 : F32 || NT > 1 ? 3 : 4)
                             wA[0] <<= 8 * (1 - (t4 & 1));
                             wB[0] <<= 8 * (1 - (t4 & 1));
                         }
-                        constexpr uint32_t one = 0xBC00BC00u;  // (-1, -1)
+                        const uint32_t one = (T->kh[1] ^ 0x8000u) * 0x10001u;  // (-c, -c)
 #pragma unroll
                         for (int k = 0; k < PR / 2; ++k) {
                             const uint32_t a0 = ((wA[0] << (PR - 1 - 2 * k)) & 0x80008000u) ^ one;

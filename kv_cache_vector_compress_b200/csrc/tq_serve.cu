@@ -14,18 +14,20 @@ namespace {
 // ------------------------------------------------------------------ preparation
 
 constexpr int kPrepThreads = 256;
-constexpr int kPrepRows = 4;   // query rows a CTA takes
-constexpr int kPrepCols = 8;   // outputs a thread takes at most: (1024 + 1024) / 256
+constexpr int kPrepRows = 8;   // query rows of a CTA
+constexpr int kPrepCols = 64;  // operands of a CTA; 4 threads share one, a quarter of the sum each
 
 struct PrepArgs {
     Prepared P;
     const void *q;
     tq_dtype dtype;
     int64_t rows;
+    int rows_in, Hkv;
     float scale;
-    int fast;
-    ServeTables *tables;
     float *qprep, *fscale;
+    // fragments of the ragged tensor-core kernel, own caches and prefix (null: not wanted)
+    uint16_t *own_frag, *pre_frag;
+    int row_block, prefix_block, prefix_blocks;
     // contexts: the caller's lengths and the prefix, as the division reads them
     const int32_t *lens;
     int B;
@@ -41,64 +43,54 @@ __device__ __forceinline__ float load_elem(const void *p, tq_dtype t, int64_t i)
     return ((const float *)p)[i];
 }
 
-// The scale sigma of the keys' codebook.  1 bit: sigma = c, so that the operand is 1.  2 bits:
-// sigma = c_1 / (1 + i / 1024) with the i for which c_2 / sigma is nearest to an fp16 number (a
-// rational approximation of their ratio: about 2^-21 off for the Gaussian law), so that one fp16
-// operand is enough for 32-bit scores.  3 bits: sigma = c_1; the operand is split in two.
-// Called by a whole warp; the same value in every lane.
-__device__ float key_sigma(const Prepared &P, int lane) {
-    const float c1 = P.cb->kc[(1 << P.kbeta) / 2];
-    if (P.kbeta != 2) return c1;
-    const double a = c1, b = P.cb->kc[3];
-    float best = INFINITY;
-    int at = 0;
-    for (int i = lane; i < 1024; i += 32) {
-        const double h = 1.0 + i * (1.0 / 1024.0), v = b / a * h;
-        const double e = fabs((double)__half2float(__double2half(v)) / v - 1.0);
-        if ((float)e < best) {
-            best = (float)e;
-            at = i;
+// Sum over this thread's quarter of the coordinates j of w[j ld] x[j][0..7], CH loads in flight.
+template <int CH>
+__device__ __forceinline__ void quarter_dot(const float *w, int64_t ld, const float *x, int count,
+                                            float (&acc)[kPrepRows]) {
+    for (int j0 = 0; j0 < count; j0 += CH) {
+        float v[CH];
+#pragma unroll
+        for (int k = 0; k < CH; ++k) v[k] = w[(j0 + k) * ld];
+#pragma unroll
+        for (int k = 0; k < CH; ++k) {
+            const float4 a = *(const float4 *)(x + (j0 + k) * kPrepRows), b = *(const float4 *)(x + (j0 + k) * kPrepRows + 4);
+            acc[0] = fmaf(v[k], a.x, acc[0]);
+            acc[1] = fmaf(v[k], a.y, acc[1]);
+            acc[2] = fmaf(v[k], a.z, acc[2]);
+            acc[3] = fmaf(v[k], a.w, acc[3]);
+            acc[4] = fmaf(v[k], b.x, acc[4]);
+            acc[5] = fmaf(v[k], b.y, acc[5]);
+            acc[6] = fmaf(v[k], b.z, acc[6]);
+            acc[7] = fmaf(v[k], b.w, acc[7]);
         }
     }
-    for (int o = 16; o > 0; o >>= 1) {
-        const float ob = __shfl_xor_sync(kFull, best, o);
-        const int oa = __shfl_xor_sync(kFull, at, o);
-        if (ob < best || (ob == best && oa < at)) {
-            best = ob;
-            at = oa;
-        }
-    }
-    return (float)(a / (1.0 + at * (1.0 / 1024.0)));
 }
 
-__device__ void split_f16(float v, uint16_t *hi, uint16_t *lo) {
-    const __half h = __float2half_rn(v);
-    *hi = __half_as_ushort(h);
-    *lo = __half_as_ushort(__float2half_rn(v - __half2float(h)));
+// Element c of a row's operands, split hi + lo, into the fragments of row r of a slice.
+__device__ __forceinline__ void put_frag(uint16_t *frag, int64_t slice, int blocks, int block, int d, int kb, int r,
+                                         int c, float v) {
+    const int ks_all = d / 16 + d / 32, nt_all = block / 4;
+    const int blk = r / block, nt = (r % block) / 4, place = frag_place(d, kb, c);
+    const int e = place & 3, t4 = (place >> 2) & 3, ks = place >> 4, gid = 2 * (r & 3);
+    uint16_t *at = frag + ((((slice * blocks + blk) * nt_all + nt) * ks_all + ks) * 32 + 4 * gid + t4) * 4 + e;
+    const __half hi = __float2half_rn(v);
+    at[0] = __half_as_ushort(hi);
+    at[16] = __half_as_ushort(__float2half_rn(v - __half2float(hi)));  // the next gid's lane, 4 lanes on
 }
 
-// q_rot = R q and sq = S q of kPrepRows rows per CTA, scaled (see the header), in fp32 by fmaf in
-// ascending j.  The last CTA writes the tables and the contexts' lengths instead.  Reads R and S
-// once per CTA from L2 (98 KB at d = 128).
+// q_rot = R q and sq = S q in fp32, scaled (see the header), as the attention kernels take them.
+// A CTA computes kPrepCols operands of kPrepRows rows: latency bound at a few rows (three dependent
+// steps: the rows, the loads of R^T in flight together, the exchange of the quarters), and at many
+// by its reads of R^T and S^T from L2.  The last CTA lays out the contexts instead.
 __global__ void __launch_bounds__(kPrepThreads) serve_prep_kernel(PrepArgs a) {
     extern __shared__ __align__(16) float qT[];  // [d][kPrepRows]
-    __shared__ float sig;
-    __shared__ uint32_t rmax[kPrepRows];
+    __shared__ float red[4][kPrepRows][kPrepCols];
+    __shared__ float rmax[kPrepRows];
     __shared__ int64_t wsum[kPrepThreads / 32];
     const Prepared &P = a.P;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int d = P.d, m = P.m, n = d + m;
     if (blockIdx.x == gridDim.x - 1) {
-        const float sigma = a.fast ? key_sigma(P, lane) : 1.f;
-        if (tid < 8) {
-            const int K = 1 << P.kbeta;
-            split_f16(tid < K ? P.cb->kc[tid] / sigma : 0.f, &a.tables->kh[tid], &a.tables->kl[tid]);
-        }
-        const int V = 1 << P.vbeta;
-        // the largest value centroid lands in [8, 16): its low half stays a normal fp16 number
-        const float tau = exp2f((float)(ilogbf(P.cb->vc[V - 1]) - 3));
-        if (tid < 16) split_f16(tid < V ? P.cb->vc[tid] / tau : 0.f, &a.tables->vh[tid], &a.tables->vl[tid]);
-        if (tid == 0) a.tables->tau = tau;
         // clamped lengths and the stages before each sequence (a block-wide scan, 256 at a time)
         int64_t before = 0;
         for (int b0 = 0; b0 < a.B; b0 += kPrepThreads) {
@@ -137,67 +129,55 @@ __global__ void __launch_bounds__(kPrepThreads) serve_prep_kernel(PrepArgs a) {
         }
         return;
     }
-    const int64_t r0 = (int64_t)blockIdx.x * kPrepRows;
+    const int cols = (n + kPrepCols - 1) / kPrepCols;
+    const int64_t r0 = (int64_t)(blockIdx.x / cols) * kPrepRows;
     const int nr = (int)min((int64_t)kPrepRows, a.rows - r0);
-    for (int e = tid; e < kPrepRows * d; e += kPrepThreads) {
-        const int r = e / d, j = e - r * d;
-        qT[j * kPrepRows + r] = r < nr ? load_elem(a.q, a.dtype, (r0 + r) * d + j) : 0.f;
-    }
-    if (tid < kPrepRows) rmax[tid] = 0u;
-    if (warp == 0) {
-        const float s = a.fast ? key_sigma(P, lane) : 1.f;
-        if (lane == 0) sig = s;
+    const int cb = (blockIdx.x % cols) * kPrepCols;
+    {  // a warp a row
+        float mx = 0.f;
+        for (int j = lane; j < d; j += 32) {
+            const float v = warp < nr ? load_elem(a.q, a.dtype, (r0 + warp) * d + j) : 0.f;
+            qT[j * kPrepRows + warp] = v;
+            mx = fmaxf(mx, fabsf(v));
+        }
+        mx = warp_max(mx);
+        if (lane == 0) rmax[warp] = mx;
     }
     __syncthreads();
-    const float gamma = sqrtf(1.5707963267948966f) / (float)m;
-    float acc[kPrepCols][kPrepRows];
-#pragma unroll
-    for (int o = 0; o < kPrepCols; ++o) {
-#pragma unroll
-        for (int r = 0; r < kPrepRows; ++r) acc[o][r] = 0.f;
-        const int c = tid + o * kPrepThreads;
+    {
+        const int c = cb + (tid & 63), q4 = tid >> 6, part = d >> 2;
+        float acc[kPrepRows] = {};
         if (c < n) {
             const float *w = c < d ? P.RT + c : P.ST + (c - d);
-            const int ld = c < d ? d : m;
-#pragma unroll 16
-            for (int j = 0; j < d; ++j) {
-                const float v = w[(int64_t)j * ld];
-                const float4 q4 = *(const float4 *)(qT + j * kPrepRows);
-                acc[o][0] = fmaf(v, q4.x, acc[o][0]);
-                acc[o][1] = fmaf(v, q4.y, acc[o][1]);
-                acc[o][2] = fmaf(v, q4.z, acc[o][2]);
-                acc[o][3] = fmaf(v, q4.w, acc[o][3]);
-            }
-            const float f = c < d ? sig : gamma;
-#pragma unroll
-            for (int r = 0; r < kPrepRows; ++r) acc[o][r] *= f;
+            const int64_t ld = c < d ? d : m;
+            w += q4 * part * ld;
+            const float *x = qT + q4 * part * kPrepRows;
+            if (part >= 32) quarter_dot<32>(w, ld, x, part, acc);
+            else quarter_dot<8>(w, ld, x, part, acc);
         }
-    }
-    // the row's exponent: the largest operand in [2^11, 2^12), far from both ends of fp16's range
-    // (its low half, 2^-11 of it, stays a normal number); rows of zeros, infinities and NaN keep 0
-    if (a.fast) {
 #pragma unroll
-        for (int r = 0; r < kPrepRows; ++r) {
-            float mx = 0.f;
-#pragma unroll
-            for (int o = 0; o < kPrepCols; ++o) mx = fmaxf(mx, fabsf(acc[o][r]));
-            mx = warp_max(mx);
-            if (lane == 0) atomicMax(&rmax[r], __float_as_uint(mx));  // nonnegative: ordered as integers
-        }
+        for (int r = 0; r < kPrepRows; ++r) red[q4][r][tid & 63] = acc[r];
     }
     __syncthreads();
+    const int r = warp;
+    if (r >= nr) return;
+    const float bound = rmax[r] * P.serve->qbound * sqrtf((float)d);
+    const int e = (bound > 0.f && bound < INFINITY) ? min(max(ilogbf(bound) - 14, -126), 126) : 0;
+    const float down = exp2f((float)-e), gamma = sqrtf(1.5707963267948966f) / (float)m, sigma = P.serve->sigma;
+    const int64_t row = r0 + r, slice = row / a.rows_in;
+    const int rr = (int)(row - slice * a.rows_in), b = (int)(slice / a.Hkv), kv = (int)(slice - (int64_t)b * a.Hkv);
+    if (lane == 0 && cb == 0) a.fscale[row] = a.scale * kLog2eF * exp2f((float)e);
 #pragma unroll
-    for (int r = 0; r < kPrepRows; ++r) {
-        if (r >= nr) break;
-        const float mx = __uint_as_float(rmax[r]);
-        const int e = (mx > 0.f && mx < INFINITY) ? min(max(ilogbf(mx) - 11, -126), 126) : 0;
-        const float down = exp2f((float)-e);
-#pragma unroll
-        for (int o = 0; o < kPrepCols; ++o) {
-            const int c = tid + o * kPrepThreads;
-            if (c < n) a.qprep[(r0 + r) * n + c] = acc[o][r] * down;
-        }
-        if (tid == 0) a.fscale[r0 + r] = a.scale * kLog2eF * exp2f((float)e);
+    for (int k = 0; k < 2; ++k) {
+        const int cc = lane + 32 * k, c = cb + cc;
+        if (c >= n) break;
+        const float v = ((red[0][r][cc] + red[1][r][cc]) + (red[2][r][cc] + red[3][r][cc])) *
+                        ((c < d ? sigma : gamma) * down);
+        if (a.qprep) a.qprep[row * n + c] = v;
+        if (a.own_frag)
+            put_frag(a.own_frag, slice, (a.rows_in + a.row_block - 1) / a.row_block, a.row_block, d, P.kbeta, rr, c, v);
+        if (a.pre_frag)
+            put_frag(a.pre_frag, kv, a.prefix_blocks, a.prefix_block, d, P.kbeta, b * a.rows_in + rr, c, v);
     }
 }
 
@@ -218,7 +198,7 @@ __global__ void __launch_bounds__(kPlThreads) ragged_plain_kernel(RaggedArgs a) 
     const int d = P.d, m = P.m, n = d + m, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     float *qs = sm, *ps = sm + n * kPlRows;
     if (tid < kMaxLevels) {
-        kcen[tid] = P.cb->kc[tid];
+        kcen[tid] = P.cb->kc[tid] / P.serve->sigma;
         vcen[tid] = P.cb->vc[tid];
     }
     const int64_t total = ragged_total(a.c);
@@ -361,12 +341,15 @@ __global__ void __launch_bounds__(kPlThreads) ragged_plain_kernel(RaggedArgs a) 
     }
 }
 
-// ------------------------------------------------------------------ merge
+// ------------------------------------------------------------------ merge and weights
 
-constexpr int kMgThreads = 128;
-constexpr int kMgRows = 4;
+constexpr int kFinThreads = 256;
+constexpr int kMgRows = 4;       // query rows of a merging CTA, two warps each
+constexpr int kMgCols = 64;      // output coordinates of a merging CTA
+constexpr int kWtTokens = 1024;  // tokens of a weighing CTA
+constexpr int kWtRows = 64;      // rows whose normalisers it holds at a time
 
-struct MergeArgs {
+struct FinishArgs {
     Prepared P;
     RaggedCache own, prefix;
     const float *own_part, *pre_part;
@@ -374,18 +357,21 @@ struct MergeArgs {
     int rows_in, Hkv;
     tq_dtype dtype;
     void *out;
-    float *lse;  // log2 of the row's sum of 2^z, or null
+    unsigned merge_ctas;  // the CTAs behind them weigh
+    const float *zbuf;
+    float *weights;
+    int chunks;  // weighing CTAs of a slice
 };
 
-// The partials of one row, one range of CTAs per cache: base + i * step.
-struct PartRange {
+// Partials of one row and cache: (N, l, -, -, o[d]) at base + i * step.
+struct Parts {
     const float *base;
     int64_t step;
     int n;
 };
 
-__device__ __forceinline__ PartRange parts_of(const RaggedCache &c, const float *part, int slice, int r, int ps) {
-    PartRange g = {nullptr, 0, 0};
+__device__ __forceinline__ Parts parts_of(const RaggedCache &c, const float *part, int slice, int r, int ps) {
+    Parts g = {nullptr, 0, 0};
     int c0, c1;
     if (c.slices > 0 && slice_ctas(c, slice, &c0, &c1)) {
         g.base = part + ((int64_t)(c0 + slice) * c.rows + r) * ps;
@@ -395,89 +381,143 @@ __device__ __forceinline__ PartRange parts_of(const RaggedCache &c, const float 
     return g;
 }
 
-// out = R^T o / l of kMgRows rows per CTA: the partials of each row are rescaled to their largest
-// reference and added in the order of the context (a warp a row), then the rows are rotated back
-// together, so that R is read once per CTA.  A row without a token is zero.
-__global__ void __launch_bounds__(kMgThreads) serve_merge_kernel(MergeArgs a) {
-    extern __shared__ __align__(16) float osm[];  // [d][kMgRows]
+// The largest reference of the partials and the sum of their l rescaled to it, over a warp.
+__device__ __forceinline__ void joint(const Parts (&g)[2], int lane, float *N, float *L) {
+    float mx = -INFINITY, s = 0.f;
+    for (int k = 0; k < 2; ++k)
+        for (int i = lane; i < g[k].n; i += 32) {
+            const float2 h = *(const float2 *)(g[k].base + i * g[k].step);
+            const float up = fmaxf(mx, h.x);
+            s = (up == -INFINITY ? 0.f : s * exp2f(mx - up)) + (h.x == -INFINITY ? 0.f : h.y * exp2f(h.x - up));
+            mx = up;
+        }
+    const float all = warp_max(mx);
+    s = mx == -INFINITY ? 0.f : s * exp2f(mx - all);
+    *N = all;
+    *L = warp_sum(s);
+}
+
+// Merging CTAs: out = R^T o / l for kMgRows rows and kMgCols coordinates.  The partials of a row are
+// rescaled to their largest reference and added, each of two warps half of them in the order of the
+// context; the rows are then rotated back together, four threads an output.  A row without a token
+// is zero.  Weighing CTAs: weights[slice][t] += sum over the slice's rows, in ascending order, of
+// 2^(z - log2 of the row's normaliser), kWtTokens tokens each; bound by the 4 rows + 8 bytes a
+// token that they move.
+__global__ void __launch_bounds__(kFinThreads) serve_finish_kernel(FinishArgs a) {
+    extern __shared__ __align__(16) float osm[];  // [2][d][kMgRows]
+    __shared__ float red[4][kMgRows][kMgCols];
+    __shared__ float lse[kWtRows];
     const int d = a.P.d, ps = partial_stride(d), tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int64_t row0 = (int64_t)blockIdx.x * kMgRows;
+    if (blockIdx.x >= a.merge_ctas) {
+        const unsigned id = blockIdx.x - a.merge_ctas;
+        const int slice = (int)(id / a.chunks), R = a.own.rows;
+        const int len = a.own.len[slice / a.own.per_seq];
+        const int t0 = (int)(id - (unsigned)slice * a.chunks) * kWtTokens + tid;
+        if (t0 - tid >= len) return;
+        float s[4] = {};
+        for (int r0 = 0; r0 < R; r0 += kWtRows) {
+            const int nr = min(kWtRows, R - r0);
+            __syncthreads();
+            for (int r = warp; r < nr; r += kFinThreads / 32) {
+                const Parts g[2] = {{nullptr, 0, 0}, parts_of(a.own, a.own_part, slice, r0 + r, ps)};
+                float N, L;
+                joint(g, lane, &N, &L);
+                if (lane == 0) lse[r] = L == 0.f ? INFINITY : N + log2f(L);
+            }
+            __syncthreads();
+            const float *z = a.zbuf + ((int64_t)slice * R + r0) * a.own.stride + t0;
+#pragma unroll 4
+            for (int r = 0; r < nr; ++r)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (t0 + k * kFinThreads < len) s[k] += exp2f(z[r * a.own.stride + k * kFinThreads] - lse[r]);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (t0 + k * kFinThreads < len) a.weights[slice * a.own.stride + t0 + k * kFinThreads] += s[k];
+        return;
+    }
+    const int cols = (d + kMgCols - 1) / kMgCols;
+    const int64_t row0 = (int64_t)(blockIdx.x / cols) * kMgRows;
+    const int cb = (blockIdx.x % cols) * kMgCols, oc = cb + (tid & 63), q4 = tid >> 6, part = d >> 2;
+    // the first of R's rows that this thread needs, on their way while the partials are merged
+    const float *w = a.P.R + (int64_t)q4 * part * d + oc;
+    float first[32];
+#pragma unroll
+    for (int k = 0; k < 32; ++k) first[k] = k < part && oc < d ? w[(int64_t)k * d] : 0.f;
     {
-        const int64_t row = row0 + warp;
-        const bool there = row < a.rows;
-        float inv = 0.f, N = -INFINITY;
-        PartRange g[2] = {{nullptr, 0, 0}, {nullptr, 0, 0}};
-        if (there) {
+        const int r4 = warp >> 1, half = warp & 1;
+        const int64_t row = row0 + r4;
+        Parts g[2] = {{nullptr, 0, 0}, {nullptr, 0, 0}};
+        if (row < a.rows) {
             const int slice = (int)(row / a.rows_in), r = (int)(row % a.rows_in);
             const int b = slice / a.Hkv, kv = slice - b * a.Hkv;
             g[0] = parts_of(a.prefix, a.pre_part, kv, b * a.rows_in + r, ps);
             g[1] = parts_of(a.own, a.own_part, slice, r, ps);
-            for (int k = 0; k < 2; ++k)
-                for (int i = lane; i < g[k].n; i += 32) N = fmaxf(N, g[k].base[i * g[k].step]);
-            N = warp_max(N);
-            float L = 0.f;
-            for (int k = 0; k < 2; ++k)
-                for (int i = lane; i < g[k].n; i += 32) {
-                    const float *p = g[k].base + i * g[k].step;
-                    L += N == -INFINITY ? 0.f : p[1] * exp2f(p[0] - N);
-                }
-            L = warp_sum(L);
-            inv = L != 0.f ? 1.f / L : 0.f;
-            if (lane == 0 && a.lse) a.lse[row] = L == 0.f ? INFINITY : N + log2f(L);
         }
-        for (int j0 = 0; j0 < d; j0 += 32) {
-            const int j = j0 + lane;
-            float acc = 0.f;
-            for (int k = 0; k < 2; ++k)
-#pragma unroll 4
-                for (int i = 0; i < g[k].n; ++i) {
-                    const float *p = g[k].base + i * g[k].step;
-                    const float w = N == -INFINITY ? 0.f : exp2f(p[0] - N);
-                    acc = fmaf(w, p[4 + j], acc);
+        float N, L;
+        joint(g, lane, &N, &L);
+        const float inv = L != 0.f ? 1.f / L : 0.f;
+        for (int j0 = 0; j0 < d; j0 += 128) {
+            const int j = j0 + 4 * lane;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int k = 0; k < 2; ++k) {
+                const int mid = (g[k].n + 1) / 2, i0 = half ? mid : 0, i1 = half ? g[k].n : mid;
+                for (int c0 = i0; c0 < i1; c0 += 32) {
+                    const int cnt = min(32, i1 - c0);
+                    float sc = 0.f;
+                    if (lane < cnt) {
+                        const float h = g[k].base[(c0 + lane) * g[k].step];
+                        sc = h == -INFINITY ? 0.f : exp2f(h - N) * inv;
+                    }
+#pragma unroll 8
+                    for (int i = 0; i < cnt; ++i) {
+                        const float f = __shfl_sync(kFull, sc, i);
+                        if (j < d) {
+                            const float4 o = *(const float4 *)(g[k].base + (c0 + i) * g[k].step + 4 + j);
+                            acc.x = fmaf(f, o.x, acc.x);
+                            acc.y = fmaf(f, o.y, acc.y);
+                            acc.z = fmaf(f, o.z, acc.z);
+                            acc.w = fmaf(f, o.w, acc.w);
+                        }
+                    }
                 }
-            osm[j * kMgRows + warp] = acc * inv;
+            }
+            if (j < d) {
+                float *o = osm + (half * d + j) * kMgRows + r4;
+                o[0] = acc.x;
+                o[kMgRows] = acc.y;
+                o[2 * kMgRows] = acc.z;
+                o[3 * kMgRows] = acc.w;
+            }
         }
     }
     __syncthreads();
-    for (int j = tid; j < d; j += kMgThreads) {
-        float acc[kMgRows] = {};
-#pragma unroll 16
-        for (int i = 0; i < d; ++i) {
-            const float v = a.P.R[(int64_t)i * d + j];
-            const float4 o4 = *(const float4 *)(osm + i * kMgRows);
-            acc[0] = fmaf(v, o4.x, acc[0]);
-            acc[1] = fmaf(v, o4.y, acc[1]);
-            acc[2] = fmaf(v, o4.z, acc[2]);
-            acc[3] = fmaf(v, o4.w, acc[3]);
-        }
+    float acc[kMgRows] = {};
+    const float4 *o0 = (const float4 *)osm + q4 * part, *o1 = o0 + d;
+    auto add = [&](float v, int k) {
+        const float4 x = o0[k], y = o1[k];
+        acc[0] = fmaf(v, x.x + y.x, acc[0]);
+        acc[1] = fmaf(v, x.y + y.y, acc[1]);
+        acc[2] = fmaf(v, x.z + y.z, acc[2]);
+        acc[3] = fmaf(v, x.w + y.w, acc[3]);
+    };
 #pragma unroll
-        for (int r = 0; r < kMgRows; ++r) {
-            if (row0 + r >= a.rows) break;
-            const int64_t at = (row0 + r) * d + j;
-            if (a.dtype == TQ_F16) ((__half *)a.out)[at] = __float2half_rn(acc[r]);
-            else if (a.dtype == TQ_BF16) ((__nv_bfloat16 *)a.out)[at] = __float2bfloat16_rn(acc[r]);
-            else ((float *)a.out)[at] = acc[r];
-        }
-    }
-}
-
-// ------------------------------------------------------------------ softmax weights
-
-constexpr int kWtThreads = 256;
-
-// weights[slice][t] += sum over the slice's rows of 2^(z - lse): one thread a token, the rows in
-// ascending order.  Bound by the 4 rows + 8 bytes a token that it moves.
-__global__ void __launch_bounds__(kWtThreads) serve_weigh_kernel(RaggedCache c, const float *__restrict__ zbuf,
-                                                                 const float *__restrict__ lse,
-                                                                 float *__restrict__ weights) {
-    const int slice = blockIdx.y;
-    const int t = blockIdx.x * kWtThreads + threadIdx.x;
-    if (t >= c.len[slice / c.per_seq]) return;
-    const float *z = zbuf + (int64_t)slice * c.rows * c.stride + t;
-    const float *L = lse + (int64_t)slice * c.rows;
-    float s = 0.f;
-    for (int r = 0; r < c.rows; ++r) s += exp2f(z[r * c.stride] - L[r]);
-    weights[slice * c.stride + t] += s;
+    for (int k = 0; k < 32; ++k)
+        if (k < part) add(first[k], k);
+    if (oc < d)
+#pragma unroll 16
+        for (int k = 32; k < part; ++k) add(w[(int64_t)k * d], k);
+#pragma unroll
+    for (int r = 0; r < kMgRows; ++r) red[q4][r][tid & 63] = acc[r];
+    __syncthreads();
+    const int r = tid >> 6;
+    if (row0 + r >= a.rows || oc >= d) return;
+    const float v = (red[0][r][tid & 63] + red[1][r][tid & 63]) + (red[2][r][tid & 63] + red[3][r][tid & 63]);
+    const int64_t at = (row0 + r) * d + oc;
+    if (a.dtype == TQ_F16) ((__half *)a.out)[at] = __float2half_rn(v);
+    else if (a.dtype == TQ_BF16) ((__nv_bfloat16 *)a.out)[at] = __float2bfloat16_rn(v);
+    else ((float *)a.out)[at] = v;
 }
 
 }  // namespace
@@ -521,9 +561,9 @@ cudaError_t launch_ragged_mma(const RaggedArgs &a, bool f32, int row_block, cuda
 
 namespace {
 // CTAs among which the stages of a cache are divided: enough to fill the GPU once together with
-// the row blocks, and no more than there are stages.
+// the row blocks, and no more than there are fours of stages (a CTA's warps take one each).
 int division(int64_t slices, int64_t cap, int64_t row_blocks, int per_sm) {
-    const int64_t most = slices * ((cap + kStage - 1) / kStage);
+    const int64_t most = slices * ((cap + 4 * kStage - 1) / (4 * kStage));
     int64_t want = (148ll * per_sm + row_blocks - 1) / row_blocks;
     if (want > most) want = most;
     return (int)(want < 1 ? 1 : want);
@@ -554,12 +594,16 @@ ServePlan plan_serve(const Prepared &P, tq_dtype dtype, int B, int Hq, int Hkv, 
         o = align_up(o + bytes, 256);
         return at;
     };
-    p.tables = take(sizeof(ServeTables));
     p.lens = take(sizeof(int32_t) * ((size_t)B + 1));
     p.cum = take(sizeof(int64_t) * ((size_t)B + 3));
-    p.qprep = take(sizeof(float) * (size_t)(rows * n));
+    p.qprep = take(p.fast ? 0 : sizeof(float) * (size_t)(rows * n));
+    // hi and lo of each operand, 2 bytes each, for whole blocks of rows
+    auto frag_bytes = [&](int64_t slices, int64_t r, int block) {
+        return (size_t)(slices * ((r + block - 1) / block) * block * n * 4);
+    };
+    p.own_frag = take(p.fast && t_cap > 0 ? frag_bytes((int64_t)B * Hkv, R, p.row_block) : 0);
+    p.pre_frag = take(p.fast && t_prefix > 0 ? frag_bytes(Hkv, (int64_t)B * R, p.prefix_block) : 0);
     p.fscale = take(sizeof(float) * (size_t)rows);
-    p.lse = take(weigh ? sizeof(float) * (size_t)rows : 0);
     p.zbuf = take(weigh ? sizeof(float) * (size_t)rows * (size_t)t_cap : 0);
     const size_t ps = sizeof(float) * partial_stride(P.d);
     p.own_part = take(p.own_ctas ? ps * ((size_t)p.own_ctas + (size_t)B * Hkv) * R : 0);
@@ -571,16 +615,23 @@ ServePlan plan_serve(const Prepared &P, tq_dtype dtype, int B, int Hq, int Hkv, 
 cudaError_t launch_serve(const ServeCall &call, const ServePlan &plan, void *scratch, cudaStream_t s) {
     char *base = (char *)scratch;
     const Prepared &P = call.P;
+    const int R = call.Hq / call.Hkv * call.Nq;
     PrepArgs pa;
+    memset(&pa, 0, sizeof(pa));
     pa.P = P;
     pa.q = call.q;
     pa.dtype = call.dtype;
     pa.rows = call.rows;
+    pa.rows_in = R;
+    pa.Hkv = call.Hkv;
     pa.scale = call.scale;
-    pa.fast = plan.fast;
-    pa.tables = (ServeTables *)(base + plan.tables);
-    pa.qprep = (float *)(base + plan.qprep);
     pa.fscale = (float *)(base + plan.fscale);
+    if (!plan.fast) pa.qprep = (float *)(base + plan.qprep);
+    if (plan.fast && plan.own_ctas) pa.own_frag = (uint16_t *)(base + plan.own_frag);
+    if (plan.fast && plan.prefix_ctas) pa.pre_frag = (uint16_t *)(base + plan.pre_frag);
+    pa.row_block = plan.row_block;
+    pa.prefix_block = plan.prefix_block;
+    pa.prefix_blocks = (int)(((int64_t)call.B * R + plan.prefix_block - 1) / plan.prefix_block);
     pa.lens = call.lens;
     pa.B = call.B;
     pa.t_cap = call.t_cap;
@@ -588,19 +639,19 @@ cudaError_t launch_serve(const ServeCall &call, const ServePlan &plan, void *scr
     pa.len_own = (int32_t *)(base + plan.lens);
     pa.cum_own = (int64_t *)(base + plan.cum);
     pa.dev_status = call.dev_status;
-    serve_prep_kernel<<<(unsigned)((call.rows + kPrepRows - 1) / kPrepRows + 1), kPrepThreads,
-                        sizeof(float) * kPrepRows * P.d, s>>>(pa);
+    const int64_t prep_ctas = (call.rows + kPrepRows - 1) / kPrepRows * ((P.d + P.m + kPrepCols - 1) / kPrepCols) + 1;
+    serve_prep_kernel<<<(unsigned)prep_ctas, kPrepThreads, sizeof(float) * kPrepRows * P.d, s>>>(pa);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
 
-    const int R = call.Hq / call.Hkv * call.Nq;
     RaggedArgs own, pre;
     memset(&own, 0, sizeof(own));
     own.P = P;
-    own.tables = pa.tables;
     own.qprep = pa.qprep;
     own.fscale = pa.fscale;
     pre = own;
+    own.frag = (const uint2 *)pa.own_frag;
+    pre.frag = (const uint2 *)pa.pre_frag;
     if (plan.own_ctas) {
         own.c = call.own;
         own.c.len = pa.len_own;
@@ -630,24 +681,28 @@ cudaError_t launch_serve(const ServeCall &call, const ServePlan &plan, void *scr
                       : launch_ragged_plain(pre, s);
         if (e != cudaSuccess) return e;
     }
-    MergeArgs ma;
-    ma.P = P;
-    ma.own = own.c;
-    ma.prefix = pre.c;
-    ma.own_part = own.part;
-    ma.pre_part = pre.part;
-    ma.rows = call.rows;
-    ma.rows_in = R;
-    ma.Hkv = call.Hkv;
-    ma.dtype = call.dtype;
-    ma.out = call.out;
-    ma.lse = call.weights ? (float *)(base + plan.lse) : nullptr;
-    serve_merge_kernel<<<(unsigned)((call.rows + kMgRows - 1) / kMgRows), kMgThreads,
-                         sizeof(float) * kMgRows * P.d, s>>>(ma);
-    e = cudaGetLastError();
-    if (e != cudaSuccess || !call.weights) return e;
-    dim3 grid((unsigned)((call.t_cap + kWtThreads - 1) / kWtThreads), (unsigned)(call.B * call.Hkv));
-    serve_weigh_kernel<<<grid, kWtThreads, 0, s>>>(own.c, own.zbuf, ma.lse, call.weights);
+    FinishArgs fa;
+    memset(&fa, 0, sizeof(fa));
+    fa.P = P;
+    fa.own = own.c;
+    fa.prefix = pre.c;
+    fa.own_part = own.part;
+    fa.pre_part = pre.part;
+    fa.rows = call.rows;
+    fa.rows_in = R;
+    fa.Hkv = call.Hkv;
+    fa.dtype = call.dtype;
+    fa.out = call.out;
+    const int64_t merge = (call.rows + kMgRows - 1) / kMgRows * ((P.d + kMgCols - 1) / kMgCols);
+    int64_t weigh = 0;
+    if (call.weights) {
+        fa.zbuf = own.zbuf;
+        fa.weights = call.weights;
+        fa.chunks = (int)((call.t_cap + kWtTokens - 1) / kWtTokens);
+        weigh = (int64_t)fa.chunks * call.B * call.Hkv;
+    }
+    fa.merge_ctas = (unsigned)merge;
+    serve_finish_kernel<<<(unsigned)(merge + weigh), kFinThreads, 2 * sizeof(float) * kMgRows * P.d, s>>>(fa);
     return cudaGetLastError();
 }
 

@@ -4,8 +4,9 @@
 // Estimated logits of query row r against token t, in log2 units:
 //   z = f_r ||k_t|| ( sum_j Q_rj C[kidx_tj] + rho_t sum_i P_ri sgn_ti )
 // Q = sigma 2^-e_r R q, P = 2^-e_r sqrt(pi/2)/m S q, C[k] = c[k] / sigma and
-// f_r = 2^e_r scale log2(e): sigma is a scale of the codebook (below), e_r one of the row, both
-// chosen so that 16-bit operands lose nothing they need.
+// f_r = 2^e_r scale log2(e).  sigma is the codebook's scale (ServeTables); e_r, one number a row,
+// puts the largest operand that R, S and the row's largest |q| allow into [2^14, 2^15), so that fp16
+// operands neither overflow nor lose their low halves.
 //
 // Softmax with the value norms inside.  With y = z + log2 ||v_t|| and a running reference
 // N >= y - 8 the weights w = 2^(y - N) are what multiplies the value centroids, and the
@@ -26,14 +27,6 @@ constexpr float kMinNorm = 5.9604644775390625e-8f;  // 2^-24
 constexpr float kLog2eF = 1.4426950408889634f;
 
 __host__ __device__ constexpr int partial_stride(int d) { return d + 4; }  // (N, l, -, -, o[d])
-
-// 16-bit operand tables of one call (fp16 bits), written by the preparation kernel.
-struct ServeTables {
-    uint16_t kh[8], kl[8];    // c_k / sigma = kh + kl for the keys' codebook
-    uint16_t vh[16], vl[16];  // c_v / tau = vh + vl for the values'
-    float tau;                // a power of two
-    float pad[3];
-};
 
 // The caches of one attention pass.  `slices` slices of records, `stride` records apart; slice s
 // belongs to sequence s / per_seq and holds len[s / per_seq] tokens.  A slice is attended by
@@ -105,6 +98,48 @@ __device__ __forceinline__ bool slice_ctas(const RaggedCache &c, int slice, int 
     return true;
 }
 
+// ---- operand order.  The sums over coordinates are free in their order, so the query operands are
+// laid out the way the kernels decode the packed words.
+
+// Register kernels (tq_ragged_mma.cuh): element e (0..3) of lane t4's operand in product ks of the
+// code part.  A lane takes whole words (half a word at 64 coordinates); nibble 4 h + e of selector i
+// holds bit 4 (4 h + e) + i of a word.  1-bit codes are taken as the signs are.
+__host__ __device__ constexpr int frag_code_coord(int D, int KB, int t4, int ks, int e) {
+    const int ng = D >= 128 ? D / 128 : 1;
+    if (KB == 1) {
+        const int pairs = D >= 128 ? 16 : 8, j = 2 * ks + (e >> 1);
+        const int g = D >= 128 ? t4 * ng + j / pairs : t4 >> 1;
+        return 32 * g + (D >= 128 ? 0 : 8 * (t4 & 1)) + j % pairs + 16 * (e & 1);
+    }
+    const int ni = D >= 128 ? 4 : 2, h = ks & 1, i = (ks >> 1) % ni;
+    const int g = D >= 128 ? t4 * ng + (ks >> 1) / ni : t4 >> 1;
+    return 32 * g + 4 * (4 * h + e) + i + (D >= 128 ? 0 : 2 * (t4 & 1));
+}
+// ... and of the sign part: pairs of bits (l, l + 16), D / 16 pairs a lane.
+__host__ __device__ constexpr int frag_sign_coord(int D, int t4, int ks, int e) {
+    const int lpw = 256 / D, pw = D / 16;
+    return 32 * (t4 / lpw) + (t4 % lpw) * pw + 2 * ks + (e >> 1) + 16 * (e & 1);
+}
+// The inverse: operand index c (codes 0 .. D-1, then signs) to 4 (4 ks + t4) + e.
+__host__ __device__ constexpr int frag_place(int D, int KB, int c) {
+    if (c >= D) {
+        const int s = c - D, lpw = 256 / D, pw = D / 16, word = s >> 5, l = s & 15, up = (s >> 4) & 1;
+        const int t4 = word * lpw + l / pw, j = l % pw;
+        return 4 * (4 * (D / 16 + j / 2) + t4) + 2 * (j & 1) + up;
+    }
+    const int g = c >> 5, bit = c & 31, ng = D >= 128 ? D / 128 : 1;
+    if (KB == 1) {
+        const int pairs = D >= 128 ? 16 : 8, l = bit & 15, up = bit >> 4;
+        const int t4 = D >= 128 ? g / ng : 2 * g + (l >> 3);
+        const int j = (D >= 128 ? (g % ng) * pairs : 0) + l % pairs;
+        return 4 * (4 * (j / 2) + t4) + 2 * (j & 1) + up;
+    }
+    const int ni = D >= 128 ? 4 : 2, nib = bit >> 2, i4 = bit & 3;
+    const int t4 = D >= 128 ? g / ng : 2 * g + (i4 >> 1), i = D >= 128 ? i4 : i4 & 1;
+    const int ks = ((D >= 128 ? g % ng : 0) * ni + i) * 2 + (nib >> 2);
+    return 4 * (4 * ks + t4) + (nib & 3);
+}
+
 // One call of tq_attend_shared or tq_attend_weigh.
 struct ServeCall {
     Prepared P;
@@ -129,7 +164,7 @@ struct ServePlan {
     int own_ctas;      // division of the own caches (0: no own caches)
     int prefix_ctas;   // division of the prefix by the ragged kernel (0: not by it)
     // byte offsets in the scratch
-    size_t tables, lens, cum, qprep, fscale, zbuf, lse, own_part, pre_part, total;
+    size_t lens, cum, qprep, own_frag, pre_frag, fscale, zbuf, own_part, pre_part, total;
 };
 
 ServePlan plan_serve(const Prepared &P, tq_dtype dtype, int B, int Hq, int Hkv, int Nq, int64_t t_prefix,
@@ -140,8 +175,8 @@ cudaError_t launch_serve(const ServeCall &call, const ServePlan &plan, void *scr
 struct RaggedArgs {
     Prepared P;
     RaggedCache c;
-    const ServeTables *tables;
-    const float *qprep;   // [rows, d + m], (Q, P) of each row
+    const float *qprep;   // plain kernel: [rows, d + m], (Q, P) of each row
+    const uint2 *frag;    // tensor cores: [slices, row blocks][row tiles of 4][products][32 lanes]
     const float *fscale;  // [rows]
     float *part;          // partials, [(ctas + slices) * c.rows, d + 4]
     float *zbuf;          // z of every (row of the slice, token): [slices, rows, stride], or null

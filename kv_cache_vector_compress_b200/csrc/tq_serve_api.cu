@@ -31,6 +31,8 @@ tq_status check_shape(tq_dtype dtype, int B, int Hq, int Hkv, int Nq, int64_t t_
     if (B < 1 || Hq < 1 || Hkv < 1 || Nq < 1 || Hq % Hkv) return TQ_ERR_INVALID_ARG;
     if (t_prefix < 0 || t_cap < 0 || t_prefix + t_cap < 1) return TQ_ERR_INVALID_ARG;
     if (t_prefix > kMaxTokens || t_cap > kMaxTokens) return TQ_ERR_UNSUPPORTED;
+    // CTAs that add up the weights of 1024 slots each
+    if ((t_cap + 1023) / 1024 * B > INT32_MAX / 2 / Hkv) return TQ_ERR_UNSUPPORTED;
     if ((int64_t)B * Hq > kMaxRowsTotal || (int64_t)B * Hq * Nq > kMaxRowsTotal) return TQ_ERR_UNSUPPORTED;
     return TQ_OK;
 }
