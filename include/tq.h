@@ -369,7 +369,7 @@ tq_status tq_attend_static(const tq_params *p, const float *q, int B, int Hq, in
  *   scratch  : tq_attend_shared_scratch_bytes(...) bytes; calls that share it must not overlap
  * Precision: with TQ_F32 the products keep 32 bits.  With the 16-bit types the operands of a
  * product are rounded to 16 bits (relative 2^-11) and sums, maxima and normalisers are in 32.
- * TQ_ERR_UNSUPPORTED when t_prefix or t_cap exceeds 2^31 - 64 or B * Hq * Nq exceeds 262140.
+ * TQ_ERR_UNSUPPORTED when t_prefix or t_cap exceeds 2^31 - 1024 or B * Hq * Nq exceeds 262140.
  */
 size_t tq_attend_shared_scratch_bytes(const tq_params *p, tq_dtype dtype, int B, int Hq, int Hkv, int Nq,
                                       int64_t t_prefix, int64_t t_cap);

@@ -28,6 +28,7 @@ struct PrepArgs {
     // fragments of the ragged tensor-core kernel, own caches and prefix (null: not wanted)
     uint16_t *own_frag, *pre_frag;
     int row_block, prefix_block, prefix_blocks;
+    uint16_t *qrows;  // rows of the many-row prefix kernel (null: not wanted)
     // contexts: the caller's lengths and the prefix, as the division reads them
     const int32_t *lens;
     int B;
@@ -176,6 +177,9 @@ __global__ void __launch_bounds__(kPrepThreads) serve_prep_kernel(PrepArgs a) {
         if (a.qprep) a.qprep[row * n + c] = v;
         if (a.own_frag)
             put_frag(a.own_frag, slice, (a.rows_in + a.row_block - 1) / a.row_block, a.row_block, d, P.kbeta, rr, c, v);
+        if (a.qrows)
+            a.qrows[((int64_t)kv * a.B * a.rows_in + (int64_t)b * a.rows_in + rr) * n + prefix_column(d, c)] =
+                __half_as_ushort(__float2half_rn(v));
         if (a.pre_frag)
             put_frag(a.pre_frag, kv, a.prefix_blocks, a.prefix_block, d, P.kbeta, b * a.rows_in + rr, c, v);
     }
@@ -353,6 +357,7 @@ struct FinishArgs {
     Prepared P;
     RaggedCache own, prefix;
     const float *own_part, *pre_part;
+    int tc_splits;  // > 0: the prefix's partials are those of the many-row kernel
     int64_t rows;
     int rows_in, Hkv;
     tq_dtype dtype;
@@ -452,7 +457,13 @@ __global__ void __launch_bounds__(kFinThreads) serve_finish_kernel(FinishArgs a)
         if (row < a.rows) {
             const int slice = (int)(row / a.rows_in), r = (int)(row % a.rows_in);
             const int b = slice / a.Hkv, kv = slice - b * a.Hkv;
-            g[0] = parts_of(a.prefix, a.pre_part, kv, b * a.rows_in + r, ps);
+            if (a.tc_splits) {
+                g[0].base = a.pre_part + ((int64_t)kv * a.prefix.rows + b * a.rows_in + r) * ps;
+                g[0].step = (int64_t)a.Hkv * a.prefix.rows * ps;
+                g[0].n = a.tc_splits;
+            } else {
+                g[0] = parts_of(a.prefix, a.pre_part, kv, b * a.rows_in + r, ps);
+            }
             g[1] = parts_of(a.own, a.own_part, slice, r, ps);
         }
         float N, L;
@@ -586,7 +597,10 @@ ServePlan plan_serve(const Prepared &P, tq_dtype dtype, int B, int Hq, int Hkv, 
         p.prefix_block = ragged_mma_rows(P, f32, (int64_t)B * R);
     }
     if (t_cap > 0) p.own_ctas = division((int64_t)B * Hkv, t_cap, (R + p.row_block - 1) / p.row_block, per_sm);
-    if (t_prefix > 0)
+    // many 16-bit rows on one prefix: the many-row kernel
+    const bool tc = p.fast && !f32 && t_prefix > 0 && (int64_t)B * R > 8;
+    if (tc) p.tc = prefix_split(P.d, Hkv, (int64_t)B * R, t_prefix);
+    else if (t_prefix > 0)
         p.prefix_ctas = division(Hkv, t_prefix, ((int64_t)B * R + p.prefix_block - 1) / p.prefix_block, per_sm);
     size_t o = 0;
     auto take = [&](size_t bytes) {
@@ -602,12 +616,14 @@ ServePlan plan_serve(const Prepared &P, tq_dtype dtype, int B, int Hq, int Hkv, 
         return (size_t)(slices * ((r + block - 1) / block) * block * n * 4);
     };
     p.own_frag = take(p.fast && t_cap > 0 ? frag_bytes((int64_t)B * Hkv, R, p.row_block) : 0);
-    p.pre_frag = take(p.fast && t_prefix > 0 ? frag_bytes(Hkv, (int64_t)B * R, p.prefix_block) : 0);
+    p.pre_frag = take(p.fast && p.prefix_ctas ? frag_bytes(Hkv, (int64_t)B * R, p.prefix_block) : 0);
+    p.qrows = take(tc ? sizeof(uint16_t) * (size_t)(rows * n) : 0);
     p.fscale = take(sizeof(float) * (size_t)rows);
     p.zbuf = take(weigh ? sizeof(float) * (size_t)rows * (size_t)t_cap : 0);
     const size_t ps = sizeof(float) * partial_stride(P.d);
     p.own_part = take(p.own_ctas ? ps * ((size_t)p.own_ctas + (size_t)B * Hkv) * R : 0);
     p.pre_part = take(p.prefix_ctas ? ps * ((size_t)p.prefix_ctas + Hkv) * (size_t)B * R : 0);
+    if (tc) p.pre_part = take(ps * (size_t)p.tc.splits * Hkv * (size_t)B * R);
     p.total = o;
     return p;
 }
@@ -629,6 +645,7 @@ cudaError_t launch_serve(const ServeCall &call, const ServePlan &plan, void *scr
     if (!plan.fast) pa.qprep = (float *)(base + plan.qprep);
     if (plan.fast && plan.own_ctas) pa.own_frag = (uint16_t *)(base + plan.own_frag);
     if (plan.fast && plan.prefix_ctas) pa.pre_frag = (uint16_t *)(base + plan.pre_frag);
+    if (plan.tc.splits) pa.qrows = (uint16_t *)(base + plan.qrows);
     pa.row_block = plan.row_block;
     pa.prefix_block = plan.prefix_block;
     pa.prefix_blocks = (int)(((int64_t)call.B * R + plan.prefix_block - 1) / plan.prefix_block);
@@ -666,7 +683,7 @@ cudaError_t launch_serve(const ServeCall &call, const ServePlan &plan, void *scr
         e = plan.fast ? launch_ragged_mma(own, call.dtype == TQ_F32, plan.row_block, s) : launch_ragged_plain(own, s);
         if (e != cudaSuccess) return e;
     }
-    if (plan.prefix_ctas) {
+    if (call.t_prefix > 0) {
         pre.c = call.prefix;
         pre.c.len = pa.len_own + call.B;
         pre.c.cum = pa.cum_own + call.B + 1;
@@ -677,8 +694,9 @@ cudaError_t launch_serve(const ServeCall &call, const ServePlan &plan, void *scr
         pre.c.rows_outer = (int64_t)call.Hkv * R;
         pre.c.ctas = plan.prefix_ctas;
         pre.part = (float *)(base + plan.pre_part);
-        e = plan.fast ? launch_ragged_mma(pre, call.dtype == TQ_F32, plan.prefix_block, s)
-                      : launch_ragged_plain(pre, s);
+        e = plan.tc.splits ? launch_prefix_tc(P, pre.c, pa.qrows, pa.fscale, pre.part, plan.tc, call.dev_status, s)
+            : plan.fast    ? launch_ragged_mma(pre, call.dtype == TQ_F32, plan.prefix_block, s)
+                           : launch_ragged_plain(pre, s);
         if (e != cudaSuccess) return e;
     }
     FinishArgs fa;
@@ -688,6 +706,7 @@ cudaError_t launch_serve(const ServeCall &call, const ServePlan &plan, void *scr
     fa.prefix = pre.c;
     fa.own_part = own.part;
     fa.pre_part = pre.part;
+    fa.tc_splits = plan.tc.splits;
     fa.rows = call.rows;
     fa.rows_in = R;
     fa.Hkv = call.Hkv;

@@ -140,6 +140,22 @@ __host__ __device__ constexpr int frag_place(int D, int KB, int c) {
     return 4 * (4 * ks + t4) + (nib & 3);
 }
 
+// Prefix kernel (tq_prefix_tc.cu): the column of operand index c (codes, then signs) in a query row.
+__host__ __device__ constexpr int prefix_column(int D, int c) {
+    const int g = c & ~31, bit = c & 31;
+    return c < D ? g + 8 * (bit & 3) + (bit >> 2) : g + 2 * (bit & 15) + (bit >> 4);
+}
+__host__ __device__ constexpr int prefix_tile(int D) { return D <= 128 ? 128 : 64; }  // tokens of a tile
+
+struct PrefixSplit {
+    int splits, tiles_per;
+};
+PrefixSplit prefix_split(int d, int Hkv, int64_t rows, int64_t t_prefix);
+// Partials [split][KV head][row] of c.rows rows on a prefix of c.stride tokens; qrows: fp16
+// [KV heads, c.rows, d + m] in prefix_column order.
+cudaError_t launch_prefix_tc(const Prepared &P, const RaggedCache &c, const uint16_t *qrows, const float *fscale,
+                             float *part, const PrefixSplit &sp, int32_t *dev_status, cudaStream_t s);
+
 // One call of tq_attend_shared or tq_attend_weigh.
 struct ServeCall {
     Prepared P;
@@ -163,8 +179,9 @@ struct ServePlan {
     int prefix_block;  // ... and the prefix
     int own_ctas;      // division of the own caches (0: no own caches)
     int prefix_ctas;   // division of the prefix by the ragged kernel (0: not by it)
+    PrefixSplit tc;    // splits of the prefix by the many-row kernel (0: not by it)
     // byte offsets in the scratch
-    size_t lens, cum, qprep, own_frag, pre_frag, fscale, zbuf, own_part, pre_part, total;
+    size_t lens, cum, qprep, own_frag, pre_frag, qrows, fscale, zbuf, own_part, pre_part, total;
 };
 
 ServePlan plan_serve(const Prepared &P, tq_dtype dtype, int B, int Hq, int Hkv, int Nq, int64_t t_prefix,

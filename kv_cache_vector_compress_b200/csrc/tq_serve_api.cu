@@ -12,7 +12,7 @@ namespace {
 
 bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
 
-constexpr int64_t kMaxTokens = (int64_t)INT32_MAX - 63;
+constexpr int64_t kMaxTokens = (int64_t)INT32_MAX - 1023;
 constexpr int64_t kMaxRowsTotal = 65535 * 4;  // blocks of four rows in a grid's second dimension
 
 tq_status check_params(const tq_params *p) {
