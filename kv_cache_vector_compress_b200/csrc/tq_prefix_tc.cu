@@ -2,11 +2,19 @@
 //
 // The rows of all sequences that read a KV head's prefix are one operand: 128 rows at a time are
 // multiplied with tiles of the prefix that are decoded once for them.
-//   S = Q B^T   128 x TT, B = TT tokens x (d + m): centroids c / sigma, then +-rho (both fp16)
-//   O += W V    128 x d,  W = 2^(y - N) in fp16, V = TT tokens x d: centroids c / tau
-// (tq_serve.cuh: y = z + log2 ||v||, the reference N, partial results.)
+//   S = Q B^T   128 x TT, B = TT tokens x (d + m): ||k|| (c / sigma), then +-||k|| rho, in fp16
+//   O += W V    128 x d,  W = the weights in fp16, V = TT tokens x d: ||v|| (c / tau) in fp16
+// The norms are multiplied into the decoded operands (on the FMA pipe, which decoding leaves idle),
+// so that a weight is one fused multiply-add and one exponential of its score.  Both are scaled by
+// powers of two, 2^k and 2^s, one of each a tile, that put the tile's largest norm in [2^10, 2^11):
+// the products stay inside fp16 whatever the norms are.  With z = f 2^-k S and a reference
+// N >= z - s - 8, W = 2^(z - s - N), and the normaliser is 2^s sum W: the partial result
+// (N, l, o) is that of tq_serve.cuh.
 //
-// Roles: four softmax warps (a thread a row), eight decoder warps, one warp that issues the MMAs.
+// Roles: eight softmax warps (two threads a row, half of a tile's tokens each), eight decoder warps,
+// one warp that issues the MMAs.  The softmax first takes the weights with the reference as it is;
+// if any comes out above 2^8 (the first tile, hardly ever later) the tile is done again with a new
+// reference, so that the usual path needs no maximum before its exponentials.
 // Q stays in tensor memory as the A operand and W is written over the scores it came from, so that
 // shared memory carries only the decoded tiles: with both operands in shared memory a 128 x 128 x 16
 // product reads 128 bytes a cycle, all that there is.  Decoded tiles are double buffered, keys and
@@ -33,7 +41,7 @@ namespace {
 using namespace sm100;
 using namespace decode;
 
-constexpr int kSmWarps = 4, kDecWarps = 8;
+constexpr int kSmWarps = 8, kDecWarps = 8;
 constexpr int kDecThreads = 32 * kDecWarps;
 constexpr int kThreads = 32 * (kSmWarps + kDecWarps + 1);
 constexpr int kSms = 148;  // grid sizing (fixed so scratch sizes do not vary)
@@ -52,10 +60,14 @@ struct Cfg {
     static constexpr uint32_t CS = 0, CO = SB * TT, CQ = CO + D;
     static_assert(CQ + K / 2 <= 512, "tensor memory");
     // shared memory
-    static constexpr uint32_t OV = 2 * KST, OM = OV + 2 * VST, META = 3 * TT * 4, OB = OM + 2 * META;
-    static constexpr uint32_t SMEM = OB + 16 * 8 + 16 + 1024;  // barriers, flags, alignment
+    static constexpr uint32_t OV = 2 * KST, OM = OV + 2 * VST, OB = OM + 2 * 16;  // OM: a tile's scales
+    static constexpr uint32_t OX = OB + 16 * 8 + 16;  // barriers, flags; exchanges of the halves
+    static constexpr uint32_t SMEM = OX + 2 * 128 * 4 + 64 + 1024;  // alignment
     // words of a decoder thread's share of a tile
-    static constexpr int KI = TT * G32 / kDecThreads, SI = (TT * SW + kDecThreads - 1) / kDecThreads;
+    static constexpr int KI = TT * G32 / kDecThreads, TP = kDecThreads / G32;  // TP tokens a pass
+    static constexpr int SWT = TT * SW;  // sign words of a tile: at most one a thread
+    static_assert(KI * TP == TT && SWT <= kDecThreads, "shares");
+    static constexpr int NL = TT / 32;  // norms of a lane in a warp's maximum over the tile
 };
 
 enum Bar { kKFull = 0, kKEmpty = 2, kVFull = 4, kVEmpty = 6, kSFull = 8, kPFull = 10 };
@@ -128,11 +140,30 @@ __device__ __forceinline__ uint64_t sdesc_mn(uint32_t saddr, uint32_t next) {
            ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
 
+// N words that start at a multiple of N words (zeros if there is nothing to read), in wide loads.
+template <int N>
+__device__ __forceinline__ void load_words(const uint32_t *p, bool in, uint32_t (&w)[N]) {
+    if constexpr (N == 2) {
+        const uint2 v = in ? *(const uint2 *)p : make_uint2(0, 0);
+        w[0] = v.x;
+        w[1] = v.y;
+    } else if constexpr (N == 4) {
+        const uint4 v = in ? *(const uint4 *)p : make_uint4(0, 0, 0, 0);
+        w[0] = v.x;
+        w[1] = v.y;
+        w[2] = v.z;
+        w[3] = v.w;
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) w[i] = in ? p[i] : 0u;
+    }
+}
+
 // What a decoder thread has fetched of one tile.
 template <class C>
 struct Share {
-    uint32_t k[C::KI][C::KB], s[C::SI], v[C::KI][C::VB];
-    uint16_t rho[C::SI], vn[C::KI], kn, mv;
+    uint32_t k[C::KI][C::KB], s, v[C::KI][C::VB];
+    uint16_t rho, kns, kn[C::KI], vn[C::KI], ka[C::NL], va[C::NL];
 };
 
 template <int D, int KB>
@@ -171,14 +202,21 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(PrefixArgs a) {
     const uint32_t tmem = *tmem_s;
 
     if (warp < kSmWarps) {
-        // ------------------------------------------------------------ softmax: a thread a row
-        const int row = rt * 128 + tid;
+        // ------------------------------------------------------------ softmax
+        // Warps w and w + 4 share the rows of lane quarter w: half h of the columns each.  They agree
+        // on the reference through shared memory and a barrier of their own.
+        constexpr int HC = TT / 2;  // columns of a thread
+        const int quarter = warp & 3, h = warp >> 2, r128 = 32 * quarter + lane;
+        const int row = rt * 128 + r128;
         const bool there = row < a.c.rows;
-        const uint32_t tl = tmem + ((uint32_t)(32 * warp) << 16);
+        const uint32_t tl = tmem + ((uint32_t)(32 * quarter) << 16);
+        float *xch = (float *)(sm + C::OX);
+        volatile int *flags = (volatile int *)(sm + C::OX + 2 * 128 * 4);  // [two tiles][half][quarter]
+        auto pair_sync = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory"); };
         {  // the query rows into tensor memory
             const uint4 *q = (const uint4 *)(a.qrows + ((int64_t)kv * a.c.rows + row) * C::K);
-#pragma unroll
-            for (int c = 0; c < C::K / 32; ++c) {
+#pragma unroll 2
+            for (int c = h; c < C::K / 32; c += 2) {
                 uint32_t v[16];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
@@ -196,103 +234,113 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(PrefixArgs a) {
             if (lane == 0) mbar_arrive(&bars[kPFull + (C::SB - 1)]);  // phase 0 of the last buffer: Q is there
         }
         const float f = there ? a.fscale[ragged_row(a.c, kv, row)] : 0.f;
-        const f2 ff = pack2(f, f);
         float N = -FLT_MAX;
         f2 l2 = pack2(0.f, 0.f);
         bool ok = true;
         for (int j = 0; j < nT; ++j) {
             const int sb = j % C::SB, vs = j & 1;
+            // a pair stays together: both take the abort flag as it is behind the barrier
             if (!mbar_wait(&bars[kVFull + vs], (j >> 1) & 1, abort_s) ||
-                !mbar_wait(&bars[kSFull + sb], (j / C::SB) & 1, abort_s)) {
+                !mbar_wait(&bars[kSFull + sb], (j / C::SB) & 1, abort_s))
                 ok = false;
-                break;
-            }
             tc_fence_after();
             const uint32_t ts = tl + C::CS + sb * TT;
-            const float *meta = (const float *)(sm + C::OM + vs * C::META);
-            // y of 32 tokens as 16 pairs
-            auto ys = [&](const uint32_t (&s)[32], int c, f2 (&y)[16]) {
-                const float4 *kn4 = (const float4 *)(meta + 32 * c), *lv4 = (const float4 *)(meta + TT + 32 * c);
+            // 2^-k, s and 2^s of the tile
+            const float4 scl = *(const float4 *)(sm + C::OM + vs * 16);
+            const f2 fk = pack2(f * scl.x, f * scl.x);
+            // tokens of this thread's columns that are there (the last tile may end early)
+            const int cols = T - (j0 + j) * TT - HC * h;
+            // the weights, as fp16 pairs, and their sum; returns the largest pair
+            uint32_t p[HC / 2];
+            f2 sum_w;
+            auto weigh = [&]() -> __half2 {
+                const f2 nn = pack2(-(N + scl.y), -(N + scl.y));
+                __half2 top = __floats2half2_rn(0.f, 0.f);
+                f2 la = pack2(0.f, 0.f), lb = la;
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const float4 kn = kn4[k], lv = lv4[k];
-                    const f2 s0 = pack2(__uint_as_float(s[4 * k]), __uint_as_float(s[4 * k + 1]));
-                    const f2 s1 = pack2(__uint_as_float(s[4 * k + 2]), __uint_as_float(s[4 * k + 3]));
-                    y[2 * k] = fma2(mul2(s0, ff), pack2(kn.x, kn.y), pack2(lv.x, lv.y));
-                    y[2 * k + 1] = fma2(mul2(s1, ff), pack2(kn.z, kn.w), pack2(lv.z, lv.w));
-                }
-            };
-            float mx = -FLT_MAX;
-            {
-                uint32_t s[2][32];
-                tmem_ld32(ts, s[0]);
-#pragma unroll
-                for (int c = 0; c < TT / 32; ++c) {
-                    ld_done(s[c & 1]);
-                    if (c + 1 < TT / 32) tmem_ld32(ts + 32 * (c + 1), s[(c + 1) & 1]);
-                    f2 y[16];
-                    ys(s[c & 1], c, y);
+                for (int c = 0; c < HC / 32; ++c) {
+                    uint32_t s[32];
+                    tmem_ld32(ts + HC * h + 32 * c, s);
+                    ld_done(s);
+                    float e[32];
 #pragma unroll
                     for (int k = 0; k < 16; ++k) {
-                        float u, v;
-                        unpack2(y[k], u, v);
-                        mx = fmaxf(mx, fmaxf(u, v));
+                        unpack2(fma2(pack2(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])), fk, nn), e[2 * k],
+                                e[2 * k + 1]);
+                    }
+                    if (cols < HC) {
+#pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            if (32 * c + k >= cols) e[k] = -INFINITY;
+                    }
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) e[k] = ex2(e[k]);
+#pragma unroll
+                    for (int k = 0; k < 16; k += 2) {
+                        la = add2(la, pack2(e[2 * k], e[2 * k + 1]));
+                        lb = add2(lb, pack2(e[2 * k + 2], e[2 * k + 3]));
+                        const __half2 h0 = __floats2half2_rn(e[2 * k], e[2 * k + 1]);
+                        const __half2 h1 = __floats2half2_rn(e[2 * k + 2], e[2 * k + 3]);
+                        top = __hmax2(top, __hmax2(h0, h1));
+                        p[16 * c + k] = *(const uint32_t *)&h0;
+                        p[16 * c + k + 1] = *(const uint32_t *)&h1;
                     }
                 }
-            }
-            if (__any_sync(kFull, mx > N + 8.f)) {
-                // move the reference: O and l to the new one (O once the last product is complete)
-                const float up = fmaxf(mx, N), sc = exp2f(N - up);
+                sum_w = add2(la, lb);
+                return top;
+            };
+            const __half2 top = weigh();
+            const bool over = fmaxf(__low2float(top), __high2float(top)) > 256.f;
+            const bool any = __any_sync(kFull, over);
+            if (lane == 0) flags[(j & 1) * 8 + 4 * h + quarter] = any || !ok;
+            tc_fence_before();
+            pair_sync();  // and both have read their scores: weights may go over them
+            if (any || !ok || flags[(j & 1) * 8 + 4 * (1 - h) + quarter]) {
+                if (*abort_s) ok = false;
+                // once more with a new reference: O and l move to it (O once the last product is complete)
+                float mx = -FLT_MAX;
+#pragma unroll 1
+                for (int c = 0; c < HC / 16; ++c) {
+                    uint32_t s[16];
+                    tmem_ld16(ts + HC * h + 16 * c, s);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int k = 0; k < 16; ++k)
+                        if (16 * c + k < cols) mx = fmaxf(mx, __uint_as_float(s[k]) * (f * scl.x) - scl.y);
+                }
+                xch[128 * h + r128] = mx;
+                pair_sync();
+                mx = fmaxf(mx, xch[128 * (1 - h) + r128]);
+                const float up = mx > N + 8.f ? mx : N, sc = exp2f(N - up);
                 N = up;
                 l2 = mul2(l2, pack2(sc, sc));
                 if (j > 0) {
-                    if (!mbar_wait(&bars[kVEmpty + ((j - 1) & 1)], ((j - 1) >> 1) & 1, abort_s)) {
-                        ok = false;
-                        break;
-                    }
+                    ok = ok && mbar_wait(&bars[kVEmpty + ((j - 1) & 1)], ((j - 1) >> 1) & 1, abort_s);
                     tc_fence_after();
 #pragma unroll 1
-                    for (int c = 0; c < D / 16; ++c) {
+                    for (int c = 0; c < D / 32; ++c) {
                         uint32_t o[16];
-                        tmem_ld16(tl + C::CO + 16 * c, o);
+                        tmem_ld16(tl + C::CO + (D / 2) * h + 16 * c, o);
                         tmem_ld_wait();
 #pragma unroll
                         for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * sc);
-                        tmem_st16(tl + C::CO + 16 * c, o);
+                        tmem_st16(tl + C::CO + (D / 2) * h + 16 * c, o);
                     }
+                }
+                weigh();
+                pair_sync();  // both have read their scores again, and the exchange
+                if (!ok || *abort_s) {
+                    ok = false;
+                    break;
                 }
             }
-            const f2 nn = pack2(-N, -N);
-            {
-                uint32_t s[2][32];
-                tmem_ld32(ts, s[0]);
+            l2 = fma2(sum_w, pack2(scl.z, scl.z), l2);
 #pragma unroll
-                for (int c = 0; c < TT / 32; ++c) {
-                    ld_done(s[c & 1]);
-                    if (c + 1 < TT / 32) tmem_ld32(ts + 32 * (c + 1), s[(c + 1) & 1]);
-                    f2 y[16];
-                    ys(s[c & 1], c, y);
-                    const float4 *rv4 = (const float4 *)(meta + 2 * TT + 32 * c);
-                    uint32_t p[16];
+            for (int c = 0; c < HC / 32; ++c) {
+                uint32_t v[16];
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const float4 rv = rv4[k];
-                        float w0, w1, w2, w3;
-                        unpack2(add2(y[2 * k], nn), w0, w1);
-                        unpack2(add2(y[2 * k + 1], nn), w2, w3);
-                        w0 = ex2(w0);
-                        w1 = ex2(w1);
-                        w2 = ex2(w2);
-                        w3 = ex2(w3);
-                        l2 = fma2(pack2(w0, w1), pack2(rv.x, rv.y), l2);
-                        l2 = fma2(pack2(w2, w3), pack2(rv.z, rv.w), l2);
-                        __half2 h0 = __floats2half2_rn(w0, w1), h1 = __floats2half2_rn(w2, w3);
-                        p[2 * k] = *(uint32_t *)&h0;
-                        p[2 * k + 1] = *(uint32_t *)&h1;
-                    }
-                    // over scores that are read already (the next chunk's are further on)
-                    tmem_st16(ts + 16 * c, p);
-                }
+                for (int k = 0; k < 16; ++k) v[k] = p[16 * c + k];
+                tmem_st16(ts + HC / 2 * h + 16 * c, v);
             }
             tmem_st_wait();
             tc_fence_before();
@@ -301,18 +349,19 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(PrefixArgs a) {
         }
         ok = ok && mbar_wait(&bars[kVEmpty + ((nT - 1) & 1)], ((nT - 1) >> 1) & 1, abort_s);
         tc_fence_after();
-        ok = __all_sync(kFull, ok);
-        if (ok) {
+        float la, lb;
+        unpack2(l2, la, lb);
+        if (h == 1) xch[r128] = la + lb;
+        pair_sync();
+        if (__all_sync(kFull, ok)) {
             float *pp = a.part + (((int64_t)split * a.c.slices + kv) * a.c.rows + row) * partial_stride(D);
-            float la, lb;
-            unpack2(l2, la, lb);
-            if (there) *(float4 *)pp = make_float4(N, la + lb, 0.f, 0.f);
+            if (there && h == 0) *(float4 *)pp = make_float4(N, la + lb + xch[r128], 0.f, 0.f);
             const float tau = a.P.serve->tau;
 #pragma unroll 1
-            for (int g = 0; g < D / 32; ++g) {
+            for (int g = h; g < D / 32; g += 2) {
                 uint32_t o[32];
                 tmem_ld32(tl + C::CO + 32 * g, o);
-                tmem_ld_wait();
+                ld_done(o);
                 if (there)
 #pragma unroll
                     for (int n = 0; n < 8; ++n)
@@ -329,98 +378,118 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(PrefixArgs a) {
         const Lut kh = load_lut<(1 << KB)>(tab->kh);
         const Lut vh = load_lut<(1 << VN)>(tab->vh + (VB == 4 ? 8 : 0));
         const int64_t rec0 = (int64_t)kv * T;
-        // word item x of a tile: eight tokens x every group, then the next eight tokens
-        auto item = [&](int x, int per, int &t, int &g) {
-            t = (x & 7) + 8 * (x / (8 * per));
-            g = (x >> 3) % per;
-        };
+        // This thread's words: of word g of tokens tk, tk + TP, ...: eight tokens (the rows of a swizzle
+        // pattern) x every word, then the next eight tokens; and sign word sg of token ts.
+        const int tk = (dt & 7) + 8 * (dt / (8 * C::G32)), g = (dt >> 3) % C::G32;
+        const int ts = (dt & 7) + 8 * (dt / (8 * C::SW)), sg = (dt >> 3) % C::SW;
+        uint32_t koff[4], soff[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            koff[u] = chunk_at<C::BLK>(tk, 4 * g + u);
+            soff[u] = chunk_at<C::BLK>(ts, D / 8 + 4 * sg + u);
+        }
         auto fetch = [&](int j, Share<C> &h) {
             const int t0 = (j0 + j) * TT;
+            const int64_t rec = rec0 + t0;
+            const uint32_t *kp = a.c.kcodes + (rec + tk) * C::KWPT + g * KB;
+            const uint32_t *vp = a.c.vcodes + (rec + tk) * C::VWPT + g * VB;
+            const uint16_t *kn = a.c.knorm + rec, *vn = a.c.vnorm + rec;
+            if (t0 + TT <= T) {
 #pragma unroll
-            for (int i = 0; i < C::KI; ++i) {
-                int t, g;
-                item(dt + i * kDecThreads, C::G32, t, g);
-                const bool in = t0 + t < T;
-                const int64_t rec = rec0 + t0 + t;
+                for (int i = 0; i < C::KI; ++i) {
+                    load_words<KB>(kp + i * C::TP * C::KWPT, true, h.k[i]);
+                    load_words<VB>(vp + i * C::TP * C::VWPT, true, h.v[i]);
+                    h.kn[i] = kn[tk + i * C::TP];
+                    h.vn[i] = vn[tk + i * C::TP];
+                }
+            } else {
 #pragma unroll
-                for (int p = 0; p < KB; ++p) h.k[i][p] = in ? a.c.kcodes[rec * C::KWPT + g * KB + p] : 0u;
-#pragma unroll
-                for (int p = 0; p < VB; ++p) h.v[i][p] = in ? a.c.vcodes[rec * C::VWPT + g * VB + p] : 0u;
-                h.vn[i] = in ? a.c.vnorm[rec] : (uint16_t)0;
+                for (int i = 0; i < C::KI; ++i) {
+                    const bool in = t0 + tk + i * C::TP < T;
+                    load_words<KB>(kp + i * C::TP * C::KWPT, in, h.k[i]);
+                    load_words<VB>(vp + i * C::TP * C::VWPT, in, h.v[i]);
+                    h.kn[i] = in ? kn[tk + i * C::TP] : (uint16_t)0;
+                    h.vn[i] = in ? vn[tk + i * C::TP] : (uint16_t)0;
+                }
             }
+            const bool in = dt < C::SWT && t0 + ts < T;
+            h.s = in ? a.c.ksigns[(rec + ts) * C::SW + sg] : 0u;
+            h.rho = in ? a.c.krnorm[rec + ts] : (uint16_t)0;
+            h.kns = in ? kn[ts] : (uint16_t)0;
 #pragma unroll
-            for (int i = 0; i < C::SI; ++i) {
-                int t, g;
-                item(dt + i * kDecThreads, C::SW, t, g);
-                const bool in = dt + i * kDecThreads < TT * C::SW && t0 + t < T;
-                h.s[i] = in ? a.c.ksigns[(rec0 + t0 + t) * C::SW + g] : 0u;
-                h.rho[i] = in ? a.c.krnorm[rec0 + t0 + t] : (uint16_t)0;
+            for (int i = 0; i < C::NL; ++i) {  // every warp takes the tile's largest norms by itself
+                const bool there = t0 + lane + 32 * i < T;
+                h.ka[i] = there ? kn[lane + 32 * i] : (uint16_t)0;
+                h.va[i] = there ? vn[lane + 32 * i] : (uint16_t)0;
             }
-            const bool in = dt < TT && t0 + dt < T;
-            h.kn = in ? a.c.knorm[rec0 + t0 + dt] : (uint16_t)0;
-            h.mv = in ? a.c.vnorm[rec0 + t0 + dt] : (uint16_t)0;
         };
-        Share<C> cur, nxt;
-        fetch(0, cur);
-        for (int j = 0; j < nT; ++j) {
+        // The exponent that puts the largest of the tile's norms into [2^10, 2^11) (fp16 bits are in
+        // the order of the numbers; 0 if all norms are 0).
+        auto exponent = [&](const uint16_t (&x)[C::NL]) -> int {
+            uint32_t mx = 0;
+#pragma unroll
+            for (int i = 0; i < C::NL; ++i) mx = max(mx, (uint32_t)(x[i] & 0x7FFFu));
+            mx = __reduce_max_sync(kFull, mx);
+            if (mx == 0) return 0;
+            return 10 - ilogbf(f16_bits_to_f32((uint16_t)min(mx, 0x7BFFu)));
+        };
+        auto pair_of = [](float v) {  // (v, v) in fp16
+            const __half2 x = __float2half2_rn(v);
+            return *(const uint32_t *)&x;
+        };
+        auto mul_pairs = [](uint4 &o, uint32_t f) {
+            const __half2 m = *(const __half2 *)&f;
+            __half2 *v = (__half2 *)&o;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[k] = __hmul2(v[k], m);
+        };
+        // decode tile j from what was fetched of it; false when a wait gave up
+        auto decode_tile = [&](int j, const Share<C> &h) -> bool {
             const int st = j & 1;
-            if (j + 1 < nT) fetch(j + 1, nxt);
-            if (j >= 2 && !mbar_wait(&bars[kKEmpty + st], ((j >> 1) - 1) & 1, abort_s)) break;
+            if (j >= 2 && !mbar_wait(&bars[kKEmpty + st], ((j >> 1) - 1) & 1, abort_s)) return false;
             uint8_t *kt = sm + st * C::KST;
+            const int ke = exponent(h.ka), ve = exponent(h.va);
+            const float kscale = exp2f((float)ke), vscale = exp2f((float)ve);
 #pragma unroll
             for (int i = 0; i < C::KI; ++i) {
-                int t, g;
-                item(dt + i * kDecThreads, C::G32, t, g);
+                const uint32_t nk = pair_of(f16_bits_to_f32(h.kn[i]) * kscale);
                 uint32_t x[4];
-                selectors<KB>(cur.k[i], x);
+                selectors<KB>(h.k[i], x);
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
                     uint4 o;
                     look_up(kh, x[u], 0u, o.x, o.y);
                     look_up(kh, x[u] >> 16, 0u, o.z, o.w);
-                    *(uint4 *)(kt + chunk_at<C::BLK>(t, 4 * g + u)) = o;
+                    mul_pairs(o, nk);
+                    *(uint4 *)(kt + koff[u] + i * C::TP * 128) = o;
                 }
             }
+            if (dt < C::SWT) {
+                const uint32_t neg = pair_of(-f16_bits_to_f32(h.rho) * (f16_bits_to_f32(h.kns) * kscale)), w = h.s;
 #pragma unroll
-            for (int i = 0; i < C::SI; ++i) {
-                int t, g;
-                item(dt + i * kDecThreads, C::SW, t, g);
-                const uint32_t neg = (uint32_t)(cur.rho[i] ^ 0x8000u) * 0x10001u, w = cur.s[i];
-                if (dt + i * kDecThreads < TT * C::SW)
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        uint4 o;
-                        o.x = ((w << (15 - 4 * u)) & 0x80008000u) ^ neg;
-                        o.y = ((w << (14 - 4 * u)) & 0x80008000u) ^ neg;
-                        o.z = ((w << (13 - 4 * u)) & 0x80008000u) ^ neg;
-                        o.w = ((w << (12 - 4 * u)) & 0x80008000u) ^ neg;
-                        *(uint4 *)(kt + chunk_at<C::BLK>(t, D / 8 + 4 * g + u)) = o;
-                    }
+                for (int u = 0; u < 4; ++u) {
+                    uint4 o;
+                    o.x = ((w << (15 - 4 * u)) & 0x80008000u) ^ neg;
+                    o.y = ((w << (14 - 4 * u)) & 0x80008000u) ^ neg;
+                    o.z = ((w << (13 - 4 * u)) & 0x80008000u) ^ neg;
+                    o.w = ((w << (12 - 4 * u)) & 0x80008000u) ^ neg;
+                    *(uint4 *)(kt + soff[u]) = o;
+                }
             }
             fence_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars[kKFull + st]);
 
-            if (j >= 2 && !mbar_wait(&bars[kVEmpty + st], ((j >> 1) - 1) & 1, abort_s)) break;
+            if (j >= 2 && !mbar_wait(&bars[kVEmpty + st], ((j >> 1) - 1) & 1, abort_s)) return false;
             uint8_t *vt = sm + C::OV + st * C::VST;
-            if (dt < TT) {
-                float *meta = (float *)(sm + C::OM + st * C::META);
-                const bool in = (j0 + j) * TT + dt < T;
-                const float v = f16_bits_to_f32(cur.mv), vc = fmaxf(v, kMinNorm);
-                meta[dt] = f16_bits_to_f32(cur.kn);
-                meta[TT + dt] = !in ? -INFINITY : v != v ? v : log2f(vc);
-                meta[2 * TT + dt] = in ? 1.f / vc : 0.f;
-            }
+            if (dt == 0)
+                *(float4 *)(sm + C::OM + st * 16) = make_float4(exp2f((float)-ke), (float)ve, exp2f((float)ve), 0.f);
 #pragma unroll
             for (int i = 0; i < C::KI; ++i) {
-                int t, g;
-                item(dt + i * kDecThreads, C::G32, t, g);
-                // a value of norm 0 (or a token past the end) is 0: an empty table
-                const bool some = (cur.vn[i] & 0x7FFFu) != 0;
-                const Lut tb = {some ? vh.h0 : 0u, some ? vh.h1 : 0u, some ? vh.l0 : 0u, some ? vh.l1 : 0u};
+                const uint32_t nv = pair_of(f16_bits_to_f32(h.vn[i]) * vscale);
                 uint32_t w[VB];
 #pragma unroll
-                for (int p = 0; p < VB; ++p) w[p] = VB == 4 && p < 3 ? ~(cur.v[i][p] ^ cur.v[i][VB - 1]) : cur.v[i][p];
+                for (int p = 0; p < VB; ++p) w[p] = VB == 4 && p < 3 ? ~(h.v[i][p] ^ h.v[i][VB - 1]) : h.v[i][p];
                 uint32_t x[4];
                 selectors<VN>(w, x);
 #pragma unroll
@@ -428,19 +497,28 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(PrefixArgs a) {
                     uint32_t f0 = 0, f1 = 0;
                     if constexpr (VB == 4) {  // the top bit is the sign
                         const uint32_t sg = (w[3] >> u) & 0x11111111u;
-                        f0 = prmt(some ? 0x80u : 0u, 0u, sg);
-                        f1 = prmt(some ? 0x80u : 0u, 0u, sg >> 16);
+                        f0 = prmt(0x80u, 0u, sg);
+                        f1 = prmt(0x80u, 0u, sg >> 16);
                     }
                     uint4 o;
-                    look_up(tb, x[u], f0, o.x, o.y);
-                    look_up(tb, x[u] >> 16, f1, o.z, o.w);
-                    *(uint4 *)(vt + chunk_at<C::BLK>(t, 4 * g + u)) = o;
+                    look_up(vh, x[u], f0, o.x, o.y);
+                    look_up(vh, x[u] >> 16, f1, o.z, o.w);
+                    mul_pairs(o, nv);
+                    *(uint4 *)(vt + koff[u] + i * C::TP * 128) = o;
                 }
             }
             fence_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars[kVFull + st]);
-            cur = nxt;
+            return true;
+        };
+        Share<C> even, odd;  // the next tile's words are fetched while one is decoded
+        fetch(0, even);
+        for (int j = 0; j < nT; j += 2) {
+            if (j + 1 < nT) fetch(j + 1, odd);
+            if (!decode_tile(j, even) || j + 1 >= nT) break;
+            if (j + 2 < nT) fetch(j + 2, even);
+            if (!decode_tile(j + 1, odd)) break;
         }
     } else if (lane == 0) {
         // ------------------------------------------------------------ MMAs
