@@ -27,8 +27,14 @@
 // out the same way by the preparation and the results put in order by the partial's writer.
 // The value tile has its d columns contiguous for each token: the B operand is MN-major.
 //
+// The packed words arrive by asynchronous copies, two tiles ahead.  (Fetched into registers a tile
+// ahead they cost twice the instructions, and the wait for one tile's words often waited for the
+// next one's too.)
+//
 // Every wait is bounded; one that runs out sets TQ_ERR_TIMEOUT in dev_status.
 #include <float.h>
+
+#include <type_traits>
 
 #include "tq_decode.cuh"
 #include "tq_serve.cuh"
@@ -62,7 +68,12 @@ struct Cfg {
     // shared memory
     static constexpr uint32_t OV = 2 * KST, OM = OV + 2 * VST, OB = OM + 2 * 16;  // OM: a tile's scales
     static constexpr uint32_t OX = OB + 16 * 8 + 16;  // barriers, flags; exchanges of the halves
-    static constexpr uint32_t SMEM = OX + 2 * 128 * 4 + 64 + 1024;  // alignment
+    // a tile's packed words: key codes, signs, value codes, then the norms from an even record on
+    static constexpr uint32_t NB = (TT + 2) * 2;
+    static constexpr uint32_t RS = TT * KWPT * 4, RV = RS + TT * SW * 4, RN = RV + TT * VWPT * 4;
+    static constexpr uint32_t RAW = (RN + 3 * NB + 15) / 16 * 16;
+    static constexpr uint32_t OR = (OX + 2 * 128 * 4 + 96 + 15) / 16 * 16;
+    static constexpr uint32_t SMEM = OR + 3 * RAW + 1024;  // alignment
     // words of a decoder thread's share of a tile
     static constexpr int KI = TT * G32 / kDecThreads, TP = kDecThreads / G32;  // TP tokens a pass
     static constexpr int SWT = TT * SW;  // sign words of a tile: at most one a thread
@@ -125,6 +136,40 @@ __device__ __forceinline__ void ld_done(uint32_t (&r)[32]) {
                  : "memory");
 }
 
+// mbar_wait in which a try may sleep for up to 4 us: the waiting warps share their schedulers with
+// the decoders, and with plain tries 3 of 10 issued instructions were theirs.
+__device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity, volatile int *abort) {
+    const uint32_t b = smem_u32(bar);
+    if (mbar_try_wait(b, parity)) return true;
+    const uint64_t t0 = globaltimer();
+    while (true) {
+        uint32_t done;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(done)
+            : "r"(b), "r"(parity), "r"(4000u)
+            : "memory");
+        if (done) return true;
+        if (*abort) return false;
+        if (globaltimer() - t0 > kTimeoutNs) {
+            *abort = 1;
+            return false;
+        }
+    }
+}
+
+// Four pairs of fp16 numbers, each times `f`, to 16 bytes of shared memory.
+__device__ __forceinline__ void store_scaled(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t f) {
+    asm volatile(
+        "{\n\t.reg .b32 x, y, z, w;\n\tmul.rn.f16x2 x, %1, %5;\n\tmul.rn.f16x2 y, %2, %5;\n\tmul.rn.f16x2 z, %3, %5;\n\t"
+        "mul.rn.f16x2 w, %4, %5;\n\tst.shared.v4.b32 [%0], {x, y, z, w};\n\t}" ::"r"(at),
+        "r"(a), "r"(b), "r"(c), "r"(d), "r"(f)
+        : "memory");
+}
+__device__ __forceinline__ void store_pairs(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 // Byte offset of 16-byte chunk c of token t in a tile of operand columns (128-byte swizzle).
@@ -140,38 +185,56 @@ __device__ __forceinline__ uint64_t sdesc_mn(uint32_t saddr, uint32_t next) {
            ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
 
-// N words that start at a multiple of N words (zeros if there is nothing to read), in wide loads.
+template <int BYTES>
+__device__ __forceinline__ void cp_async(void *dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_u32(dst)), "l"(src), "n"(BYTES) : "memory");
+}
+
+// One decoder's share of the copies of an array of W words a record: every kDecThreads-th piece of a
+// tile, the widest that every record is aligned to.
+template <int W, int TT>
+struct Copier {
+    static constexpr int G = W % 4 == 0 ? 4 : W % 2 == 0 ? 2 : 1;
+    static constexpr int PIECES = TT * W / G, N = (PIECES + kDecThreads - 1) / kDecThreads;
+    const uint32_t *src;  // this thread's first piece of the next tile
+    __device__ __forceinline__ void start(const uint32_t *array, int64_t rec, int dt) { src = array + rec * W + dt * G; }
+    // the next tile, `cnt` records of it
+    __device__ __forceinline__ void copy(uint8_t *dst, int cnt, int dt) {
+        const int have = cnt == TT ? PIECES : cnt * W / G;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int c = dt + i * kDecThreads;
+            if (c < have) cp_async<4 * G>(dst + c * G * 4, src + i * kDecThreads * G);
+        }
+        src += TT * W;
+    }
+};
+
+// N words of shared memory at a multiple of N words.
 template <int N>
-__device__ __forceinline__ void load_words(const uint32_t *p, bool in, uint32_t (&w)[N]) {
+__device__ __forceinline__ void read_words(const uint32_t *p, uint32_t (&w)[N]) {
     if constexpr (N == 2) {
-        const uint2 v = in ? *(const uint2 *)p : make_uint2(0, 0);
+        const uint2 v = *(const uint2 *)p;
         w[0] = v.x;
         w[1] = v.y;
     } else if constexpr (N == 4) {
-        const uint4 v = in ? *(const uint4 *)p : make_uint4(0, 0, 0, 0);
+        const uint4 v = *(const uint4 *)p;
         w[0] = v.x;
         w[1] = v.y;
         w[2] = v.z;
         w[3] = v.w;
     } else {
 #pragma unroll
-        for (int i = 0; i < N; ++i) w[i] = in ? p[i] : 0u;
+        for (int i = 0; i < N; ++i) w[i] = p[i];
     }
 }
-
-// What a decoder thread has fetched of one tile.
-template <class C>
-struct Share {
-    uint32_t k[C::KI][C::KB], s, v[C::KI][C::VB];
-    uint16_t rho, kns, kn[C::KI], vn[C::KI], ka[C::NL], va[C::NL];
-};
 
 template <int D, int KB>
 __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(PrefixArgs a) {
     using C = Cfg<D, KB>;
     constexpr int VB = C::VB, VN = C::VN, TT = C::TT;
     extern __shared__ uint8_t raw[];
-    uint8_t *sm = (uint8_t *)(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
+    uint8_t *sm = raw + (1024 - (smem_u32(raw) & 1023)) % 1024;  // (an offset: the address space stays known)
     uint64_t *bars = (uint64_t *)(sm + C::OB);
     volatile int *abort_s = (volatile int *)(sm + C::OB + 16 * 8);
     uint32_t *tmem_s = (uint32_t *)(sm + C::OB + 16 * 8 + 8);
@@ -211,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(PrefixArgs a) {
         const bool there = row < a.c.rows;
         const uint32_t tl = tmem + ((uint32_t)(32 * quarter) << 16);
         float *xch = (float *)(sm + C::OX);
-        volatile int *flags = (volatile int *)(sm + C::OX + 2 * 128 * 4);  // [two tiles][half][quarter]
+        volatile int *flags = (volatile int *)(sm + C::OX + 2 * 128 * 4);  // [two tiles, gave up][half][quarter]
         auto pair_sync = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory"); };
         {  // the query rows into tensor memory
             const uint4 *q = (const uint4 *)(a.qrows + ((int64_t)kv * a.c.rows + row) * C::K);
@@ -239,9 +302,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(PrefixArgs a) {
         bool ok = true;
         for (int j = 0; j < nT; ++j) {
             const int sb = j % C::SB, vs = j & 1;
-            // a pair stays together: both take the abort flag as it is behind the barrier
-            if (!mbar_wait(&bars[kVFull + vs], (j >> 1) & 1, abort_s) ||
-                !mbar_wait(&bars[kSFull + sb], (j / C::SB) & 1, abort_s))
+            // a pair of warps stays together: one that gave up says so and leaves with the other
+            if (!wait_for(&bars[kVFull + vs], (j >> 1) & 1, abort_s) ||
+                !wait_for(&bars[kSFull + sb], (j / C::SB) & 1, abort_s))
                 ok = false;
             tc_fence_after();
             const uint32_t ts = tl + C::CS + sb * TT;
@@ -296,7 +359,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(PrefixArgs a) {
             tc_fence_before();
             pair_sync();  // and both have read their scores: weights may go over them
             if (any || !ok || flags[(j & 1) * 8 + 4 * (1 - h) + quarter]) {
-                if (*abort_s) ok = false;
                 // once more with a new reference: O and l move to it (O once the last product is complete)
                 float mx = -FLT_MAX;
 #pragma unroll 1
@@ -315,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(PrefixArgs a) {
                 N = up;
                 l2 = mul2(l2, pack2(sc, sc));
                 if (j > 0) {
-                    ok = ok && mbar_wait(&bars[kVEmpty + ((j - 1) & 1)], ((j - 1) >> 1) & 1, abort_s);
+                    ok = ok && wait_for(&bars[kVEmpty + ((j - 1) & 1)], ((j - 1) >> 1) & 1, abort_s);
                     tc_fence_after();
 #pragma unroll 1
                     for (int c = 0; c < D / 32; ++c) {
@@ -328,8 +390,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(PrefixArgs a) {
                     }
                 }
                 weigh();
+                if (lane == 0) flags[16 + 4 * h + quarter] = !ok;
                 pair_sync();  // both have read their scores again, and the exchange
-                if (!ok || *abort_s) {
+                if (!ok || flags[16 + 4 * (1 - h) + quarter]) {
                     ok = false;
                     break;
                 }
@@ -347,7 +410,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(PrefixArgs a) {
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars[kPFull + sb]);
         }
-        ok = ok && mbar_wait(&bars[kVEmpty + ((nT - 1) & 1)], ((nT - 1) >> 1) & 1, abort_s);
+        ok = ok && wait_for(&bars[kVEmpty + ((nT - 1) & 1)], ((nT - 1) >> 1) & 1, abort_s);
         tc_fence_after();
         float la, lb;
         unpack2(l2, la, lb);
@@ -378,6 +441,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(PrefixArgs a) {
         const Lut kh = load_lut<(1 << KB)>(tab->kh);
         const Lut vh = load_lut<(1 << VN)>(tab->vh + (VB == 4 ? 8 : 0));
         const int64_t rec0 = (int64_t)kv * T;
+        const uint32_t sbase = smem_u32(sm);
         // This thread's words: of word g of tokens tk, tk + TP, ...: eight tokens (the rows of a swizzle
         // pattern) x every word, then the next eight tokens; and sign word sg of token ts.
         const int tk = (dt & 7) + 8 * (dt / (8 * C::G32)), g = (dt >> 3) % C::G32;
@@ -388,108 +452,124 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(PrefixArgs a) {
             koff[u] = chunk_at<C::BLK>(tk, 4 * g + u);
             soff[u] = chunk_at<C::BLK>(ts, D / 8 + 4 * sg + u);
         }
-        auto fetch = [&](int j, Share<C> &h) {
-            const int t0 = (j0 + j) * TT;
-            const int64_t rec = rec0 + t0;
-            const uint32_t *kp = a.c.kcodes + (rec + tk) * C::KWPT + g * KB;
-            const uint32_t *vp = a.c.vcodes + (rec + tk) * C::VWPT + g * VB;
-            const uint16_t *kn = a.c.knorm + rec, *vn = a.c.vnorm + rec;
-            if (t0 + TT <= T) {
-#pragma unroll
-                for (int i = 0; i < C::KI; ++i) {
-                    load_words<KB>(kp + i * C::TP * C::KWPT, true, h.k[i]);
-                    load_words<VB>(vp + i * C::TP * C::VWPT, true, h.v[i]);
-                    h.kn[i] = kn[tk + i * C::TP];
-                    h.vn[i] = vn[tk + i * C::TP];
+        Copier<C::KWPT, TT> ck;
+        Copier<C::SW, TT> cs;
+        Copier<C::VWPT, TT> cv;
+        const int64_t first = rec0 + (int64_t)j0 * TT;
+        ck.start(a.c.kcodes, first, dt);
+        cs.start(a.c.ksigns, first, dt);
+        cv.start(a.c.vcodes, first, dt);
+        // Norms in words of two, from the even record at or below a tile's first (tiles are even, so
+        // the parity is the same for all); a word that would pass the end of the array as its one half
+        // that is there.  The first 128 threads copy the keys' two, the others the values'.
+        static_assert(TT / 2 + 1 <= 128, "norm words");
+        const int odd = (int)(first & 1), nw = dt & 127;
+        const uint16_t *n0 = (dt < 128 ? a.c.knorm : a.c.vnorm) + first - odd + 2 * nw;
+        const uint16_t *n1 = a.c.krnorm + first - odd + 2 * nw;
+        int64_t n_at = first - odd + 2 * nw;
+        const uint32_t nd = C::RN + (dt < 128 ? 0 : 2 * C::NB) + 4 * nw;
+        auto issue = [&](int j, int slot) {
+            if (j < nT) {
+                const int cnt = min(TT, T - (j0 + j) * TT);
+                uint8_t *r = sm + C::OR + (uint32_t)slot * C::RAW;
+                ck.copy(r, cnt, dt);
+                cs.copy(r + C::RS, cnt, dt);
+                cv.copy(r + C::RV, cnt, dt);
+                if (nw < (odd + cnt + 1) >> 1) {
+                    if (n_at + 2 <= a.c.records) {
+                        cp_async<4>(r + nd, n0);
+                        if (dt < 128) cp_async<4>(r + nd + C::NB, n1);
+                    } else {
+                        *(uint16_t *)(r + nd) = *n0;
+                        if (dt < 128) *(uint16_t *)(r + nd + C::NB) = *n1;
+                    }
                 }
-            } else {
-#pragma unroll
-                for (int i = 0; i < C::KI; ++i) {
-                    const bool in = t0 + tk + i * C::TP < T;
-                    load_words<KB>(kp + i * C::TP * C::KWPT, in, h.k[i]);
-                    load_words<VB>(vp + i * C::TP * C::VWPT, in, h.v[i]);
-                    h.kn[i] = in ? kn[tk + i * C::TP] : (uint16_t)0;
-                    h.vn[i] = in ? vn[tk + i * C::TP] : (uint16_t)0;
-                }
+                n0 += TT;
+                n1 += TT;
+                n_at += TT;
             }
-            const bool in = dt < C::SWT && t0 + ts < T;
-            h.s = in ? a.c.ksigns[(rec + ts) * C::SW + sg] : 0u;
-            h.rho = in ? a.c.krnorm[rec + ts] : (uint16_t)0;
-            h.kns = in ? kn[ts] : (uint16_t)0;
-#pragma unroll
-            for (int i = 0; i < C::NL; ++i) {  // every warp takes the tile's largest norms by itself
-                const bool there = t0 + lane + 32 * i < T;
-                h.ka[i] = there ? kn[lane + 32 * i] : (uint16_t)0;
-                h.va[i] = there ? vn[lane + 32 * i] : (uint16_t)0;
-            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
         };
-        // The exponent that puts the largest of the tile's norms into [2^10, 2^11) (fp16 bits are in
-        // the order of the numbers; 0 if all norms are 0).
-        auto exponent = [&](const uint16_t (&x)[C::NL]) -> int {
+        // The exponent field of the largest of the tile's norms, at least 1 (fp16 bits are in the order
+        // of the numbers; infinities and NaN count as the largest number).  Every warp takes it itself.
+        auto top_field = [&](const uint16_t *n, int cnt) -> int {
             uint32_t mx = 0;
 #pragma unroll
-            for (int i = 0; i < C::NL; ++i) mx = max(mx, (uint32_t)(x[i] & 0x7FFFu));
-            mx = __reduce_max_sync(kFull, mx);
-            if (mx == 0) return 0;
-            return 10 - ilogbf(f16_bits_to_f32((uint16_t)min(mx, 0x7BFFu)));
+            for (int i = 0; i < TT / 32; ++i)
+                if (lane + 32 * i < cnt) mx = max(mx, (uint32_t)(n[lane + 32 * i] & 0x7FFFu));
+            mx = __reduce_max_sync(kFull, mx) >> 10;
+            return min(max((int)mx, 1), 30);
         };
+        auto power = [](int e) { return __int_as_float((127 + e) << 23); };
         auto pair_of = [](float v) {  // (v, v) in fp16
             const __half2 x = __float2half2_rn(v);
             return *(const uint32_t *)&x;
         };
-        auto mul_pairs = [](uint4 &o, uint32_t f) {
-            const __half2 m = *(const __half2 *)&f;
-            __half2 *v = (__half2 *)&o;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) v[k] = __hmul2(v[k], m);
-        };
-        // decode tile j from what was fetched of it; false when a wait gave up
-        auto decode_tile = [&](int j, const Share<C> &h) -> bool {
-            const int st = j & 1;
-            if (j >= 2 && !mbar_wait(&bars[kKEmpty + st], ((j >> 1) - 1) & 1, abort_s)) return false;
-            uint8_t *kt = sm + st * C::KST;
-            const int ke = exponent(h.ka), ve = exponent(h.va);
-            const float kscale = exp2f((float)ke), vscale = exp2f((float)ve);
+        // Decode tile j.  A warp whose wait gave up still takes part in the barriers, which the others wait at.
+        bool live = true;
+        int slot = 0;  // j % 3
+        auto decode_tile = [&](int j, auto stage) {
+            constexpr int st = decltype(stage)::value;  // j % 2
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
+            // every decoder's copies of this tile have landed, and the last tile's words are read
+            asm volatile("bar.sync 5, %0;" ::"n"(kDecThreads) : "memory");
+            issue(j + 2, slot == 0 ? 2 : slot - 1);
+            const uint8_t *r = sm + C::OR + (uint32_t)slot * C::RAW;
+            slot = slot == 2 ? 0 : slot + 1;
+            const int cnt = min(TT, T - (j0 + j) * TT);
+            const uint16_t *rn = (const uint16_t *)(r + C::RN) + odd;
+            const uint16_t *rkn = rn, *rkr = rn + C::NB / 2, *rvn = rn + C::NB;
+            live = live && (j < 2 || wait_for(&bars[kKEmpty + st], ((j >> 1) - 1) & 1, abort_s));
+            if (!live) return;
+            const uint32_t kt = sbase + st * C::KST;
+            // the norms' exponent is field - 15; 2^ke and 2^ve put it at 10
+            const int ke = 25 - top_field(rkn, cnt), ve = 25 - top_field(rvn, cnt);
+            const float kscale = power(ke), vscale = power(ve);
 #pragma unroll
             for (int i = 0; i < C::KI; ++i) {
-                const uint32_t nk = pair_of(f16_bits_to_f32(h.kn[i]) * kscale);
-                uint32_t x[4];
-                selectors<KB>(h.k[i], x);
+                const int tok = tk + i * C::TP;
+                // a token past the end: the norm is 0, and so is its row
+                const uint32_t nk = pair_of(tok < cnt ? f16_bits_to_f32(rkn[tok]) * kscale : 0.f);
+                uint32_t w[KB], x[4];
+                read_words<KB>((const uint32_t *)r + tok * C::KWPT + g * KB, w);
+                selectors<KB>(w, x);
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
-                    uint4 o;
-                    look_up(kh, x[u], 0u, o.x, o.y);
-                    look_up(kh, x[u] >> 16, 0u, o.z, o.w);
-                    mul_pairs(o, nk);
-                    *(uint4 *)(kt + koff[u] + i * C::TP * 128) = o;
+                    uint32_t a0, a1, a2, a3;
+                    look_up(kh, x[u], 0u, a0, a1);
+                    look_up(kh, x[u] >> 16, 0u, a2, a3);
+                    store_scaled(kt + koff[u] + i * C::TP * 128, a0, a1, a2, a3, nk);
                 }
             }
             if (dt < C::SWT) {
-                const uint32_t neg = pair_of(-f16_bits_to_f32(h.rho) * (f16_bits_to_f32(h.kns) * kscale)), w = h.s;
+                const uint32_t neg =
+                    pair_of(ts < cnt ? -f16_bits_to_f32(rkr[ts]) * (f16_bits_to_f32(rkn[ts]) * kscale) : 0.f);
+                const uint32_t w = ((const uint32_t *)(r + C::RS))[ts * C::SW + sg];
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    uint4 o;
-                    o.x = ((w << (15 - 4 * u)) & 0x80008000u) ^ neg;
-                    o.y = ((w << (14 - 4 * u)) & 0x80008000u) ^ neg;
-                    o.z = ((w << (13 - 4 * u)) & 0x80008000u) ^ neg;
-                    o.w = ((w << (12 - 4 * u)) & 0x80008000u) ^ neg;
-                    *(uint4 *)(kt + soff[u]) = o;
-                }
+                for (int u = 0; u < 4; ++u)
+                    store_pairs(kt + soff[u], ((w << (15 - 4 * u)) & 0x80008000u) ^ neg,
+                                ((w << (14 - 4 * u)) & 0x80008000u) ^ neg, ((w << (13 - 4 * u)) & 0x80008000u) ^ neg,
+                                ((w << (12 - 4 * u)) & 0x80008000u) ^ neg);
             }
             fence_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars[kKFull + st]);
 
-            if (j >= 2 && !mbar_wait(&bars[kVEmpty + st], ((j >> 1) - 1) & 1, abort_s)) return false;
-            uint8_t *vt = sm + C::OV + st * C::VST;
+            live = j < 2 || wait_for(&bars[kVEmpty + st], ((j >> 1) - 1) & 1, abort_s);
+            if (!live) return;
+            const uint32_t vt = sbase + C::OV + st * C::VST;
             if (dt == 0)
-                *(float4 *)(sm + C::OM + st * 16) = make_float4(exp2f((float)-ke), (float)ve, exp2f((float)ve), 0.f);
+                *(float4 *)(sm + C::OM + st * 16) = make_float4(power(-ke), (float)ve, vscale, 0.f);
 #pragma unroll
             for (int i = 0; i < C::KI; ++i) {
-                const uint32_t nv = pair_of(f16_bits_to_f32(h.vn[i]) * vscale);
+                const int tok = tk + i * C::TP;
+                const uint32_t nv = pair_of(tok < cnt ? f16_bits_to_f32(rvn[tok]) * vscale : 0.f);
                 uint32_t w[VB];
+                read_words<VB>((const uint32_t *)(r + C::RV) + tok * C::VWPT + g * VB, w);
+                if constexpr (VB == 4) {
 #pragma unroll
-                for (int p = 0; p < VB; ++p) w[p] = VB == 4 && p < 3 ? ~(h.v[i][p] ^ h.v[i][VB - 1]) : h.v[i][p];
+                    for (int p = 0; p < 3; ++p) w[p] = ~(w[p] ^ w[3]);
+                }
                 uint32_t x[4];
                 selectors<VN>(w, x);
 #pragma unroll
@@ -500,33 +580,30 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(PrefixArgs a) {
                         f0 = prmt(0x80u, 0u, sg);
                         f1 = prmt(0x80u, 0u, sg >> 16);
                     }
-                    uint4 o;
-                    look_up(vh, x[u], f0, o.x, o.y);
-                    look_up(vh, x[u] >> 16, f1, o.z, o.w);
-                    mul_pairs(o, nv);
-                    *(uint4 *)(vt + koff[u] + i * C::TP * 128) = o;
+                    uint32_t a0, a1, a2, a3;
+                    look_up(vh, x[u], f0, a0, a1);
+                    look_up(vh, x[u] >> 16, f1, a2, a3);
+                    store_scaled(vt + koff[u] + i * C::TP * 128, a0, a1, a2, a3, nv);
                 }
             }
             fence_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars[kVFull + st]);
-            return true;
         };
-        Share<C> even, odd;  // the next tile's words are fetched while one is decoded
-        fetch(0, even);
+        issue(0, 0);
+        issue(1, 1);
         for (int j = 0; j < nT; j += 2) {
-            if (j + 1 < nT) fetch(j + 1, odd);
-            if (!decode_tile(j, even) || j + 1 >= nT) break;
-            if (j + 2 < nT) fetch(j + 2, even);
-            if (!decode_tile(j + 1, odd)) break;
+            decode_tile(j, std::integral_constant<int, 0>{});
+            if (j + 1 < nT) decode_tile(j + 1, std::integral_constant<int, 1>{});
         }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
     } else if (lane == 0) {
         // ------------------------------------------------------------ MMAs
         const uint32_t sbase = smem_u32(sm);
         constexpr uint32_t is = idesc_f16_f32(128, TT), iv = idesc_f16_f32(128, D) | (1u << 16);
         auto scores = [&](int j) -> bool {
             const int st = j & 1, sb = j % C::SB;
-            if (!mbar_wait(&bars[kKFull + st], (j >> 1) & 1, abort_s)) return false;
+            if (!wait_for(&bars[kKFull + st], (j >> 1) & 1, abort_s)) return false;
             tc_fence_after();
             const uint32_t kb = sbase + st * C::KST;
 #pragma unroll
@@ -538,14 +615,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(PrefixArgs a) {
             return true;
         };
         // Q arrived as phase 0 of the last score buffer's W barrier
-        bool ok = mbar_wait(&bars[kPFull + (C::SB - 1)], 0, abort_s) && scores(0);
+        bool ok = wait_for(&bars[kPFull + (C::SB - 1)], 0, abort_s) && scores(0);
         for (int j = 0; ok && j < nT; ++j) {
             const int st = j & 1, sb = j % C::SB;
             // the next scores go over the weights of tile j - 1: once their product is complete
             if (C::SB == 2 && j + 1 < nT)
-                ok = (j == 0 || mbar_wait(&bars[kVEmpty + ((j - 1) & 1)], ((j - 1) >> 1) & 1, abort_s)) && scores(j + 1);
+                ok = (j == 0 || wait_for(&bars[kVEmpty + ((j - 1) & 1)], ((j - 1) >> 1) & 1, abort_s)) && scores(j + 1);
             const uint32_t ph = (uint32_t)(j / C::SB + (sb == C::SB - 1 ? 1 : 0)) & 1;
-            ok = ok && mbar_wait(&bars[kVFull + st], (j >> 1) & 1, abort_s) && mbar_wait(&bars[kPFull + sb], ph, abort_s);
+            ok = ok && wait_for(&bars[kVFull + st], (j >> 1) & 1, abort_s) && wait_for(&bars[kPFull + sb], ph, abort_s);
             if (!ok) break;
             tc_fence_after();
             const uint32_t vb = sbase + C::OV + st * C::VST;
@@ -555,7 +632,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(PrefixArgs a) {
                        (j | k) ? 1u : 0u);
             mma_commit(&bars[kVEmpty + st]);
             if (C::SB == 1 && j + 1 < nT)
-                ok = mbar_wait(&bars[kVEmpty + st], (j >> 1) & 1, abort_s) && scores(j + 1);
+                ok = wait_for(&bars[kVEmpty + st], (j >> 1) & 1, abort_s) && scores(j + 1);
         }
     }
     __syncthreads();
