@@ -620,7 +620,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(PrefixArgs a) {
             const int st = j & 1, sb = j % C::SB;
             // the next scores go over the weights of tile j - 1: once their product is complete
             if (C::SB == 2 && j + 1 < nT)
-                ok = (j == 0 || wait_for(&bars[kVEmpty + ((j - 1) & 1)], ((j - 1) >> 1) & 1, abort_s)) && scores(j + 1);
+                ok = scores(j + 1);
             const uint32_t ph = (uint32_t)(j / C::SB + (sb == C::SB - 1 ? 1 : 0)) & 1;
             ok = ok && wait_for(&bars[kVFull + st], (j >> 1) & 1, abort_s) && wait_for(&bars[kPFull + sb], ph, abort_s);
             if (!ok) break;
