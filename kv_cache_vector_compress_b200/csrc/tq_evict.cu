@@ -24,9 +24,15 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
     return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
-// One CTA per slice.
+// One CTA per slice; a thread holds up to KPT keys in registers, loaded at once, so that the slice is
+// read once while it has at most KPT x 1024 tokens (longer ones in rounds, read again from L2 by each
+// step).  Three histograms in shared memory find the threshold; then every warp's counts of each group of 32
+// keys are scanned together, which gives each key its place.
+template <int KPT>
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictCall c) {
+    constexpr int ROUND = KPT * kSelThreads;
     __shared__ uint32_t hist[kBins];
+    __shared__ uint32_t cnt[KPT * kSelWarps];  // [group of a round][warp]: keys above | keys equal << 16
     __shared__ uint32_t wsum[kSelWarps];
     __shared__ uint32_t s_digit, s_rank;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -49,17 +55,31 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictCall c) 
     }
     const float *w = (const float *)c.src[6] + (int64_t)slice * c.t_cap;
     const int safe = n - (int)c.recent;  // slots from here on are kept
-    auto key_at = [&](int t) { return t >= safe ? 0xFFFFFFFFu : weight_key(w[t]); };
+    const int rounds = (n - 1) / ROUND + 1;
+    uint32_t key[KPT];
+    auto load = [&](int round) {
+        const int t0 = round * ROUND + tid;
+        float v[KPT];
+#pragma unroll
+        for (int i = 0; i < KPT; ++i) v[i] = t0 + i * kSelThreads < n ? w[t0 + i * kSelThreads] : 0.f;
+#pragma unroll
+        for (int i = 0; i < KPT; ++i) key[i] = t0 + i * kSelThreads >= safe ? 0xFFFFFFFFu : weight_key(v[i]);
+    };
+    load(0);
     // the threshold: the keep-th largest key, found 11, 11 and 10 bits at a time
     uint32_t prefix = 0, mask = 0, rank = (uint32_t)keep;  // the rank-th largest of the keys that match
+#pragma unroll 1
     for (int pass = 0; pass < 3; ++pass) {
         const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
         const uint32_t dm = pass < 2 ? 2047u : 1023u;
         for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
         __syncthreads();
-        for (int t = tid; t < n; t += kSelThreads) {
-            const uint32_t k = key_at(t);
-            if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & dm], 1u);
+        for (int r = 0; r < rounds; ++r) {
+            if (rounds > 1) load(r);
+            const int t0 = r * ROUND + tid;
+#pragma unroll
+            for (int i = 0; i < KPT; ++i)
+                if (t0 + i * kSelThreads < n && (key[i] & mask) == prefix) atomicAdd(&hist[(key[i] >> shift) & dm], 1u);
         }
         __syncthreads();
         // suffix sums over the bins, two a thread, from the top: thread 0 takes the highest two
@@ -85,30 +105,50 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictCall c) 
         prefix |= s_digit << shift;
         mask |= dm << shift;
         rank = s_rank;
-        __syncthreads();
     }
     // kept: keys above the threshold, and the first `rank` slots whose key equals it
     uint32_t gt_before = 0, eq_before = 0;
-    for (int t0 = 0; t0 < n; t0 += kSelThreads) {
-        const int t = t0 + tid;
-        const uint32_t k = t < n ? key_at(t) : 0u;
-        const uint32_t gt = t < n && k > prefix, eq = t < n && k == prefix;
-        uint32_t x = gt | (eq << 16);
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t y = __shfl_up_sync(kFull, x, o);
-            if (lane >= o) x += y;
+    for (int r = 0; r < rounds; ++r) {
+        if (rounds > 1) load(r);
+        const int t0 = r * ROUND + tid;
+        uint32_t gt[KPT], eq[KPT];
+#pragma unroll
+        for (int i = 0; i < KPT; ++i) {
+            const bool there = t0 + i * kSelThreads < n;
+            gt[i] = __ballot_sync(kFull, there && key[i] > prefix);
+            eq[i] = __ballot_sync(kFull, there && key[i] == prefix);
+            if (lane == 0) cnt[i * kSelWarps + warp] = __popc(gt[i]) | ((uint32_t)__popc(eq[i]) << 16);
         }
-        if (lane == 31) wsum[warp] = x;
         __syncthreads();
-        uint32_t off = 0, all = 0;
-        for (int u = 0; u < kSelWarps; ++u) {
-            const uint32_t v = wsum[u];
-            if (u < warp) off += v;
-            all += v;
+        // exclusive prefix sums of the counts in slot order, KPT a thread in the first 32 warps' lanes
+        uint32_t all = 0;
+        {
+            const uint32_t x = tid < KPT * kSelWarps ? cnt[tid] : 0u;
+            uint32_t s = x;
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t y = __shfl_up_sync(kFull, s, o);
+                if (lane >= o) s += y;
+            }
+            if (lane == 31) wsum[warp] = s;
+            __syncthreads();
+            uint32_t off = 0;
+            for (int u = 0; u < kSelWarps; ++u) {
+                const uint32_t v = wsum[u];
+                if (u < warp) off += v;
+                all += v;
+            }
+            if (tid < KPT * kSelWarps) cnt[tid] = off + s - x;
         }
-        x += off - (gt | (eq << 16));  // before this thread
-        const uint32_t ngt = gt_before + (x & 0xFFFFu), neq = eq_before + (x >> 16);
-        if (gt || (eq && neq < rank)) kept[ngt + min(neq, rank)] = t;
+        __syncthreads();
+        const uint32_t below = (1u << lane) - 1u;
+#pragma unroll
+        for (int i = 0; i < KPT; ++i) {
+            const uint32_t base = cnt[i * kSelWarps + warp];
+            const uint32_t ngt = gt_before + (base & 0xFFFFu) + __popc(gt[i] & below);
+            const uint32_t neq = eq_before + (base >> 16) + __popc(eq[i] & below);
+            if (((gt[i] >> lane) & 1u) || (((eq[i] >> lane) & 1u) && neq < rank))
+                kept[ngt + min(neq, rank)] = t0 + i * kSelThreads;
+        }
         gt_before += all & 0xFFFFu;
         eq_before += all >> 16;
         __syncthreads();
@@ -117,42 +157,78 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictCall c) 
 
 constexpr int kCopyThreads = 256;
 
+// `per` words of type T a record: every thread takes pieces in turn, four loads on their way at once.
 template <typename T>
 __device__ __forceinline__ void copy_records(const void *src, void *dst, int per, int64_t src0, int64_t dst0,
                                              const int32_t *idx, int cnt, int tid) {
-    const T *s = (const T *)src;
-    T *o = (T *)dst;
-    for (int e = tid; e < cnt * per; e += kCopyThreads) {
-        const int j = e / per, k = e - j * per;
-        o[(dst0 + j) * per + k] = s[(src0 + idx[j]) * per + k];
+    const T *s = (const T *)src + src0 * per;
+    T *o = (T *)dst + dst0 * per;
+    const int all = cnt * per;
+    for (int e0 = tid; e0 < all; e0 += 4 * kCopyThreads) {
+        T v[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int e = e0 + u * kCopyThreads, j = e / per;
+            if (e < all) v[u] = s[(int64_t)idx[j] * per + (e - j * per)];
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int e = e0 + u * kCopyThreads;
+            if (e < all) o[e] = v[u];
+        }
     }
 }
 
-// kCopySlots kept records of one slice per CTA, array by array, in the widest words that every
-// record of the array is aligned to.
+__device__ __forceinline__ void copy_wide(const EvictCall &c, int a, int64_t src0, int64_t dst0, const int32_t *idx,
+                                          int cnt, int tid) {
+    const int by = c.bytes[a];
+    if (by % 16 == 0) copy_records<uint4>(c.src[a], c.dst[a], by / 16, src0, dst0, idx, cnt, tid);
+    else if (by % 8 == 0) copy_records<uint2>(c.src[a], c.dst[a], by / 8, src0, dst0, idx, cnt, tid);
+    else copy_records<uint32_t>(c.src[a], c.dst[a], by / 4, src0, dst0, idx, cnt, tid);
+}
+
+// kCopySlots kept records of one slice per CTA, a thread a record for the norms and weights, and the
+// widest words that every record is aligned to for the packed arrays.  Bound by the bytes moved.
 __global__ void __launch_bounds__(kCopyThreads) evict_copy_kernel(EvictCall c, int chunks) {
+    static_assert(kCopySlots == kCopyThreads, "a thread a record");
     __shared__ int32_t idx[kCopySlots];
     const int slice = blockIdx.x / chunks, tid = threadIdx.x;
     const int j0 = (blockIdx.x - slice * chunks) * kCopySlots;
     const int cnt = min(kCopySlots, c.counts[slice] - j0);
     if (cnt <= 0) return;
-    if (tid < cnt) idx[tid] = c.kept[(int64_t)slice * c.budget + j0 + tid];
-    __syncthreads();
     const int64_t src0 = (int64_t)slice * c.t_cap, dst0 = (int64_t)slice * c.out_cap + j0;
-    for (int a = 0; a < kEvictArrays; ++a) {
-        const int by = c.bytes[a];
-        if (by % 16 == 0) copy_records<uint4>(c.src[a], c.dst[a], by / 16, src0, dst0, idx, cnt, tid);
-        else if (by % 8 == 0) copy_records<uint2>(c.src[a], c.dst[a], by / 8, src0, dst0, idx, cnt, tid);
-        else if (by % 4 == 0) copy_records<uint32_t>(c.src[a], c.dst[a], by / 4, src0, dst0, idx, cnt, tid);
-        else copy_records<uint16_t>(c.src[a], c.dst[a], by / 2, src0, dst0, idx, cnt, tid);
+    if (tid < cnt) {
+        const int32_t i = c.kept[(int64_t)slice * c.budget + j0 + tid];
+        idx[tid] = i;
+        const int64_t s = src0 + i, o = dst0 + tid;
+        const uint16_t kn = ((const uint16_t *)c.src[2])[s], kr = ((const uint16_t *)c.src[3])[s];
+        const uint16_t vn = ((const uint16_t *)c.src[5])[s];
+        const uint32_t wt = ((const uint32_t *)c.src[6])[s];
+        ((uint16_t *)c.dst[2])[o] = kn;
+        ((uint16_t *)c.dst[3])[o] = kr;
+        ((uint16_t *)c.dst[5])[o] = vn;
+        ((uint32_t *)c.dst[6])[o] = wt;
     }
+    __syncthreads();
+    copy_wide(c, 4, src0, dst0, idx, cnt, tid);
+    copy_wide(c, 0, src0, dst0, idx, cnt, tid);
+    copy_wide(c, 1, src0, dst0, idx, cnt, tid);
+}
+
+template <int KPT>
+cudaError_t launch_select(const EvictCall &c, cudaStream_t s) {
+    evict_select_kernel<KPT><<<(unsigned)(c.B * c.Hkv), kSelThreads, 0, s>>>(c);
+    return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_evict(const EvictCall &c, cudaStream_t s) {
-    evict_select_kernel<<<(unsigned)(c.B * c.Hkv), kSelThreads, 0, s>>>(c);
-    cudaError_t e = cudaGetLastError();
+    // as few keys a thread as hold the longest slice in one round
+    const cudaError_t e = c.t_cap <= 2 * kSelThreads    ? launch_select<2>(c, s)
+                          : c.t_cap <= 8 * kSelThreads  ? launch_select<8>(c, s)
+                          : c.t_cap <= 16 * kSelThreads ? launch_select<16>(c, s)
+                                                        : launch_select<32>(c, s);
     if (e != cudaSuccess) return e;
     const int chunks = (int)evict_chunks(c.budget);
     evict_copy_kernel<<<(unsigned)(chunks * c.B * c.Hkv), kCopyThreads, 0, s>>>(c, chunks);

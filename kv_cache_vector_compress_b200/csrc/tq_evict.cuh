@@ -19,7 +19,7 @@ struct EvictCall {
     int32_t *dev_status;
 };
 
-constexpr int kCopySlots = 64;  // destination slots a CTA copies
+constexpr int kCopySlots = 256;  // destination slots a CTA copies
 inline int64_t evict_chunks(int64_t budget) { return (budget + kCopySlots - 1) / kCopySlots; }
 inline size_t evict_scratch_bytes(int B, int Hkv) { return align_up(sizeof(int32_t) * (size_t)B * Hkv, 256); }
 cudaError_t launch_evict(const EvictCall &c, cudaStream_t s);

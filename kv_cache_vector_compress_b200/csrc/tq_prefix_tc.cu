@@ -50,7 +50,6 @@ using namespace decode;
 constexpr int kSmWarps = 8, kDecWarps = 8;
 constexpr int kDecThreads = 32 * kDecWarps;
 constexpr int kThreads = 32 * (kSmWarps + kDecWarps + 1);
-constexpr int kSms = 148;  // grid sizing (fixed so scratch sizes do not vary)
 
 template <int D, int KB_>
 struct Cfg {
@@ -618,7 +617,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(PrefixArgs a) {
         bool ok = wait_for(&bars[kPFull + (C::SB - 1)], 0, abort_s) && scores(0);
         for (int j = 0; ok && j < nT; ++j) {
             const int st = j & 1, sb = j % C::SB;
-            // the next scores go over the weights of tile j - 1: once their product is complete
+            // The next scores go over the weights of tile j - 1, behind their product: one thread's MMAs
+            // run in the order in which they are issued.
             if (C::SB == 2 && j + 1 < nT)
                 ok = scores(j + 1);
             const uint32_t ph = (uint32_t)(j / C::SB + (sb == C::SB - 1 ? 1 : 0)) & 1;
@@ -646,8 +646,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(PrefixArgs a) {
 template <int D, int KB>
 cudaError_t launch_one(const PrefixArgs &a, int row_tiles, cudaStream_t s) {
     using C = Cfg<D, KB>;
-    cudaError_t e = cudaFuncSetAttribute(prefix_tc_kernel<D, KB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)C::SMEM);
+    cudaError_t e = allow_smem((const void *)prefix_tc_kernel<D, KB>, C::SMEM);
     if (e != cudaSuccess) return e;
     dim3 grid((unsigned)(a.splits * a.c.slices), (unsigned)row_tiles);
     prefix_tc_kernel<D, KB><<<grid, kThreads, C::SMEM, s>>>(a);

@@ -83,23 +83,27 @@ __device__ __forceinline__ void copy_words(void *dst, const uint32_t *src, int w
         if (c * G < words) cp_async<4 * G>((uint32_t *)dst + c * G, src + c * G);
 }
 
-// One CTA: its pieces of the slices (tq_serve.cuh) for query rows [ROWS blockIdx.y, ...).  Each warp
+// One CTA: its pieces of the slices (tq_serve.cuh) for one block of ROWS query rows.  Each warp
 // takes every NW-th stage of a piece through its own ring of asynchronous copies and keeps its own
 // reference, sums and accumulators; they meet at the end of the piece.
 //
 // The reference N of a row moves only when some y exceeds it by more than 8: then the accumulators
 // are rescaled (rare after the first stages), so that the usual path has no reduction over lanes.
 template <int D, int KB, int NT, bool F32>
-__global__ void __launch_bounds__(NW * 32, D >= 256 ? 3 : F32 || NT > 1 ? 3 : 4) ragged_mma_kernel(RaggedArgs a) {
+__global__ void __launch_bounds__(NW * 32, D >= 256 ? 3 : F32 || NT > 1 ? 3 : 4) ragged_mma_kernel(const __grid_constant__ RaggedPair pair) {
     using C = Cfg<D, KB, NT, F32>;
     constexpr int VB = C::VB, VN = VB < 3 ? VB : 3;
     extern __shared__ __align__(16) uint8_t smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gid = lane >> 2, t4 = lane & 3;
+    const bool second = (int)blockIdx.x >= pair.first;
+    const RaggedArgs &a = pair.a[second];
+    const int id = (int)blockIdx.x - (second ? pair.first : 0), cta = id % a.c.ctas, rblk = id / a.c.ctas;
+    const int rblks = (a.c.rows + C::ROWS - 1) / C::ROWS;
     const int64_t total = ragged_total(a.c);
-    const int64_t w1 = cta_first(total, a.c.ctas, blockIdx.x + 1);
-    int64_t w = cta_first(total, a.c.ctas, blockIdx.x);
+    const int64_t w1 = cta_first(total, a.c.ctas, cta + 1);
+    int64_t w = cta_first(total, a.c.ctas, cta);
     if (w >= w1) return;
-    const int r0 = blockIdx.y * C::ROWS, nr = min(C::ROWS, a.c.rows - r0);
+    const int r0 = rblk * C::ROWS, nr = min(C::ROWS, a.c.rows - r0);
     const ServeTables *T = a.P.serve;
     const Lut kh = load_lut<(1 << KB)>(T->kh);
     const Lut kl = load_lut<KB == 3 ? 8 : 1>(T->kl);
@@ -118,31 +122,6 @@ __global__ void __launch_bounds__(NW * 32, D >= 256 ? 3 : F32 || NT > 1 ? 3 : 4)
     for (; w < w1; w += pc.s1 - pc.s0) {
         pc = piece_at(a.c, w, w1);
         __syncthreads();  // the last piece's merge is read
-        // ---- query fragments of the slice
-        const uint2 *qf = a.frag + ((int64_t)pc.slice * gridDim.y + blockIdx.y) * (NT * C::KS * 32);
-        uint2 breg[C::BREG ? NT * C::KS : 1];
-        if constexpr (C::BREG) {
-#pragma unroll
-            for (int k = 0; k < NT * C::KS; ++k) breg[k] = qf[k * 32 + lane];
-        } else {
-            for (int e = tid; e < NT * C::KS * 32; e += NW * 32) bfrag[e] = qf[e];
-        }
-        float f[NT], N[NT], l[NT], o[C::NO][C::TILES][4];
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            const int row = 4 * t + t4;
-            f[t] = row < nr ? a.fscale[ragged_row(a.c, pc.slice, r0 + row)] : 0.f;
-            N[t] = -FLT_MAX;
-            l[t] = 0.f;
-        }
-#pragma unroll
-        for (int t = 0; t < C::NO; ++t)
-#pragma unroll
-            for (int i = 0; i < C::TILES; ++i)
-#pragma unroll
-                for (int k = 0; k < 4; ++k) o[t][i][k] = 0.f;
-        if constexpr (!C::BREG) __syncthreads();
-
         // ---- the warp's stages: pc.s0 + warp, + NW, ...
         const int64_t rec0 = pc.slice * a.c.stride;
         auto issue = [&](int64_t s) {
@@ -169,6 +148,31 @@ __global__ void __launch_bounds__(NW * 32, D >= 256 ? 3 : F32 || NT > 1 ? 3 : 4)
 #pragma unroll
         for (int k = 0; k < C::NST - 1; ++k) issue(first + k * NW);
         norms(first);
+        // ---- query fragments of the slice
+        const uint2 *qf = a.frag + ((int64_t)pc.slice * rblks + rblk) * (NT * C::KS * 32);
+        uint2 breg[C::BREG ? NT * C::KS : 1];
+        if constexpr (C::BREG) {
+#pragma unroll
+            for (int k = 0; k < NT * C::KS; ++k) breg[k] = qf[k * 32 + lane];
+        } else {
+            for (int e = tid; e < NT * C::KS * 32; e += NW * 32) bfrag[e] = qf[e];
+        }
+        float f[NT], N[NT], l[NT], o[C::NO][C::TILES][4];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            const int row = 4 * t + t4;
+            f[t] = row < nr ? a.fscale[ragged_row(a.c, pc.slice, r0 + row)] : 0.f;
+            N[t] = -FLT_MAX;
+            l[t] = 0.f;
+        }
+#pragma unroll
+        for (int t = 0; t < C::NO; ++t)
+#pragma unroll
+            for (int i = 0; i < C::TILES; ++i)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) o[t][i][k] = 0.f;
+        if constexpr (!C::BREG) __syncthreads();
+
         for (int64_t s = first; s < pc.s1; s += NW) {
             __syncwarp();  // every lane has read the stage whose slot is filled next, and its norms
             issue(s + (C::NST - 1) * NW);
@@ -449,7 +453,7 @@ __global__ void __launch_bounds__(NW * 32, D >= 256 ? 3 : F32 || NT > 1 ? 3 : 4)
                 s = fmaf(sc, mo[((size_t)u * C::ROWS + r) * D + j], s);
                 L = fmaf(sc, mrg[(u * C::ROWS + r) * 2 + 1], L);
             }
-            float *pp = a.part + ((int64_t)(blockIdx.x + pc.slice) * a.c.rows + r0 + r) * partial_stride(D);
+            float *pp = a.part + ((int64_t)(cta + pc.slice) * a.c.rows + r0 + r) * partial_stride(D);
             pp[4 + j] = s * tau;
             if (j == 0) {
                 pp[0] = Nm;
@@ -460,22 +464,20 @@ __global__ void __launch_bounds__(NW * 32, D >= 256 ? 3 : F32 || NT > 1 ? 3 : 4)
 }
 
 template <int D, int KB, int NT, bool F32>
-cudaError_t launch_one(const RaggedArgs &a, cudaStream_t s) {
+cudaError_t launch_one(const RaggedPair &a, cudaStream_t s) {
     using C = Cfg<D, KB, NT, F32>;
-    cudaError_t e = cudaFuncSetAttribute(ragged_mma_kernel<D, KB, NT, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)C::SMEM);
+    cudaError_t e = allow_smem((const void *)ragged_mma_kernel<D, KB, NT, F32>, C::SMEM);
     if (e != cudaSuccess) return e;
-    dim3 grid((unsigned)a.c.ctas, (unsigned)((a.c.rows + C::ROWS - 1) / C::ROWS));
-    ragged_mma_kernel<D, KB, NT, F32><<<grid, NW * 32, C::SMEM, s>>>(a);
+    ragged_mma_kernel<D, KB, NT, F32><<<(unsigned)a.total, NW * 32, C::SMEM, s>>>(a);
     return cudaGetLastError();
 }
 
 // The instances of one head dimension; defined in tq_ragged_<D>.cu.
 template <int D>
-cudaError_t launch_dim(const RaggedArgs &a, bool f32, int row_block, cudaStream_t s);
+cudaError_t launch_dim(const RaggedPair &a, bool f32, int row_block, cudaStream_t s);
 
 template <int D, int KB>
-cudaError_t launch_bits(const RaggedArgs &a, bool f32, int row_block, cudaStream_t s) {
+cudaError_t launch_bits(const RaggedPair &a, bool f32, int row_block, cudaStream_t s) {
     if (f32) {
         if constexpr (D < 256) {
             if (row_block == 8) return launch_one<D, KB, 2, true>(a, s);
@@ -487,8 +489,8 @@ cudaError_t launch_bits(const RaggedArgs &a, bool f32, int row_block, cudaStream
 
 #define TQ_RAGGED_DIM(D)                                                                              \
     template <>                                                                                       \
-    cudaError_t launch_dim<D>(const RaggedArgs &a, bool f32, int row_block, cudaStream_t s) {         \
-        switch (a.P.kbeta) {                                                                          \
+    cudaError_t launch_dim<D>(const RaggedPair &a, bool f32, int row_block, cudaStream_t s) {         \
+        switch (a.a[0].P.kbeta) {                                                                          \
             case 1: return launch_bits<D, 1>(a, f32, row_block, s);                                   \
             case 2: return launch_bits<D, 2>(a, f32, row_block, s);                                   \
             case 3: return launch_bits<D, 3>(a, f32, row_block, s);                                   \

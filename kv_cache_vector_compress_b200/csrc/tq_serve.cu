@@ -3,6 +3,9 @@
 // addition of the softmax weights; and the plain kernel for the shapes without a tensor-core one.
 #include <math.h>
 
+#include <atomic>
+#include <cstring>
+
 #include <cuda_bf16.h>
 
 #include "tq_serve.cuh"
@@ -27,7 +30,7 @@ struct PrepArgs {
     float *qprep, *fscale;
     // fragments of the ragged tensor-core kernel, own caches and prefix (null: not wanted)
     uint16_t *own_frag, *pre_frag;
-    int row_block, prefix_block, prefix_blocks;
+    int row_block, prefix_blocks;
     uint16_t *qrows;  // rows of the many-row prefix kernel (null: not wanted)
     // contexts: the caller's lengths and the prefix, as the division reads them
     const int32_t *lens;
@@ -181,7 +184,7 @@ __global__ void __launch_bounds__(kPrepThreads) serve_prep_kernel(PrepArgs a) {
             a.qrows[((int64_t)kv * a.B * a.rows_in + (int64_t)b * a.rows_in + rr) * n + prefix_column(d, c)] =
                 __half_as_ushort(__float2half_rn(v));
         if (a.pre_frag)
-            put_frag(a.pre_frag, kv, a.prefix_blocks, a.prefix_block, d, P.kbeta, b * a.rows_in + rr, c, v);
+            put_frag(a.pre_frag, kv, a.prefix_blocks, a.row_block, d, P.kbeta, b * a.rows_in + rr, c, v);
     }
 }
 
@@ -347,9 +350,9 @@ __global__ void __launch_bounds__(kPlThreads) ragged_plain_kernel(RaggedArgs a) 
 
 // ------------------------------------------------------------------ merge and weights
 
-constexpr int kFinThreads = 256;
-constexpr int kMgRows = 4;       // query rows of a merging CTA, two warps each
-constexpr int kMgCols = 64;      // output coordinates of a merging CTA
+constexpr int kFinThreads = 512;
+constexpr int kMgRows = 8;       // query rows of a merging CTA, two warps each
+constexpr int kMgParts = 8;      // partials of a row on their way at once
 constexpr int kWtTokens = 1024;  // tokens of a weighing CTA
 constexpr int kWtRows = 64;      // rows whose normalisers it holds at a time
 
@@ -386,76 +389,85 @@ __device__ __forceinline__ Parts parts_of(const RaggedCache &c, const float *par
     return g;
 }
 
-// The largest reference of the partials and the sum of their l rescaled to it, over a warp.
-__device__ __forceinline__ void joint(const Parts (&g)[2], int lane, float *N, float *L) {
+// log2 of the sum of 2^z over a row's partials; +infinity when there is nothing.  A whole warp.
+__device__ __forceinline__ float log_sum(const Parts &g, int lane) {
     float mx = -INFINITY, s = 0.f;
-    for (int k = 0; k < 2; ++k)
-        for (int i = lane; i < g[k].n; i += 32) {
-            const float2 h = *(const float2 *)(g[k].base + i * g[k].step);
-            const float up = fmaxf(mx, h.x);
-            s = (up == -INFINITY ? 0.f : s * exp2f(mx - up)) + (h.x == -INFINITY ? 0.f : h.y * exp2f(h.x - up));
-            mx = up;
-        }
+    for (int i = lane; i < g.n; i += 32) {
+        const float2 h = *(const float2 *)(g.base + i * g.step);
+        const float up = fmaxf(mx, h.x);
+        s = (up == -INFINITY ? 0.f : s * exp2f(mx - up)) + (h.x == -INFINITY ? 0.f : h.y * exp2f(h.x - up));
+        mx = up;
+    }
     const float all = warp_max(mx);
-    s = mx == -INFINITY ? 0.f : s * exp2f(mx - all);
-    *N = all;
-    *L = warp_sum(s);
+    s = warp_sum(mx == -INFINITY ? 0.f : s * exp2f(mx - all));
+    return s == 0.f ? INFINITY : all + log2f(s);
 }
 
-// Merging CTAs: out = R^T o / l for kMgRows rows and kMgCols coordinates.  The partials of a row are
-// rescaled to their largest reference and added, each of two warps half of them in the order of the
-// context; the rows are then rotated back together, four threads an output.  A row without a token
-// is zero.  Weighing CTAs: weights[slice][t] += sum over the slice's rows, in ascending order, of
-// 2^(z - log2 of the row's normaliser), kWtTokens tokens each; bound by the 4 rows + 8 bytes a
-// token that they move.
+// weights[slice][t] += sum over the slice's rows, in ascending order, of 2^(z - log2 of the row's
+// normaliser), kWtTokens tokens a CTA; bound by the 4 rows + 8 bytes a token that it moves.
+template <int THREADS>
+__device__ __forceinline__ void weigh_tokens(const FinishArgs &a, unsigned id, float *lse) {
+    constexpr int PT = kWtTokens / THREADS;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, ps = partial_stride(a.P.d);
+    const int slice = (int)(id / a.chunks), R = a.own.rows;
+    const int len = a.own.len[slice / a.own.per_seq];
+    const int t0 = (int)(id - (unsigned)slice * a.chunks) * kWtTokens + tid;
+    if (t0 - tid >= len) return;
+    float s[PT] = {};
+    for (int r0 = 0; r0 < R; r0 += kWtRows) {
+        const int nr = min(kWtRows, R - r0);
+        __syncthreads();
+        for (int r = warp; r < nr; r += THREADS / 32) {
+            const float x = log_sum(parts_of(a.own, a.own_part, slice, r0 + r, ps), lane);
+            if (lane == 0) lse[r] = x;
+        }
+        __syncthreads();
+        const float *z = a.zbuf + ((int64_t)slice * R + r0) * a.own.stride + t0;
+#pragma unroll 4
+        for (int r = 0; r < nr; ++r)
+#pragma unroll
+            for (int k = 0; k < PT; ++k)
+                if (t0 + k * THREADS < len) s[k] += exp2f(z[r * a.own.stride + k * THREADS] - lse[r]);
+    }
+#pragma unroll
+    for (int k = 0; k < PT; ++k)
+        if (t0 + k * THREADS < len) a.weights[slice * a.own.stride + t0 + k * THREADS] += s[k];
+}
+
+constexpr int kWtThreads = 256;
+
+__global__ void __launch_bounds__(kWtThreads) serve_weigh_kernel(FinishArgs a) {
+    __shared__ float lse[kWtRows];
+    weigh_tokens<kWtThreads>(a, blockIdx.x, lse);
+}
+
+// Merging CTAs: out = R^T o / l for kMgRows rows.  Two warps a row add its partials, each half of
+// them in the order of the context, rescaled to their largest reference as they come; the rows are
+// then rotated back together, several threads an output.  A row without a token is zero.
+// Latency bound at a few rows: the partials' and R's loads are issued before anything waits.
 __global__ void __launch_bounds__(kFinThreads) serve_finish_kernel(FinishArgs a) {
     extern __shared__ __align__(16) float osm[];  // [2][d][kMgRows]
-    __shared__ float red[4][kMgRows][kMgCols];
-    __shared__ float lse[kWtRows];
-    const int d = a.P.d, ps = partial_stride(d), tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    __shared__ float red[kFinThreads * kMgRows];
+    __shared__ float2 head[2][kMgRows];
     if (blockIdx.x >= a.merge_ctas) {
-        const unsigned id = blockIdx.x - a.merge_ctas;
-        const int slice = (int)(id / a.chunks), R = a.own.rows;
-        const int len = a.own.len[slice / a.own.per_seq];
-        const int t0 = (int)(id - (unsigned)slice * a.chunks) * kWtTokens + tid;
-        if (t0 - tid >= len) return;
-        float s[4] = {};
-        for (int r0 = 0; r0 < R; r0 += kWtRows) {
-            const int nr = min(kWtRows, R - r0);
-            __syncthreads();
-            for (int r = warp; r < nr; r += kFinThreads / 32) {
-                const Parts g[2] = {{nullptr, 0, 0}, parts_of(a.own, a.own_part, slice, r0 + r, ps)};
-                float N, L;
-                joint(g, lane, &N, &L);
-                if (lane == 0) lse[r] = L == 0.f ? INFINITY : N + log2f(L);
-            }
-            __syncthreads();
-            const float *z = a.zbuf + ((int64_t)slice * R + r0) * a.own.stride + t0;
-#pragma unroll 4
-            for (int r = 0; r < nr; ++r)
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    if (t0 + k * kFinThreads < len) s[k] += exp2f(z[r * a.own.stride + k * kFinThreads] - lse[r]);
-        }
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-            if (t0 + k * kFinThreads < len) a.weights[slice * a.own.stride + t0 + k * kFinThreads] += s[k];
+        weigh_tokens<kFinThreads>(a, blockIdx.x - a.merge_ctas, red);
         return;
     }
-    const int cols = (d + kMgCols - 1) / kMgCols;
-    const int64_t row0 = (int64_t)(blockIdx.x / cols) * kMgRows;
-    const int cb = (blockIdx.x % cols) * kMgCols, oc = cb + (tid & 63), q4 = tid >> 6, part = d >> 2;
-    // the first of R's rows that this thread needs, on their way while the partials are merged
-    const float *w = a.P.R + (int64_t)q4 * part * d + oc;
+    const int d = a.P.d, ps = partial_stride(d), tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int64_t row0 = (int64_t)blockIdx.x * kMgRows;
+    // this thread's column(s) of R^T o and its share of the sum
+    const int ncol = min(d, kFinThreads), ks = kFinThreads / ncol, part = d / ks;
+    const int col = tid % ncol, i0 = tid / ncol * part;
+    const float *w = a.P.R + (int64_t)i0 * d + col;
     float first[32];
 #pragma unroll
-    for (int k = 0; k < 32; ++k) first[k] = k < part && oc < d ? w[(int64_t)k * d] : 0.f;
+    for (int k = 0; k < 32; ++k) first[k] = k < part ? w[(int64_t)k * d] : 0.f;
     {
-        const int r4 = warp >> 1, half = warp & 1;
-        const int64_t row = row0 + r4;
+        const int r8 = warp >> 1, half = warp & 1;
+        const int64_t row = row0 + r8;
         Parts g[2] = {{nullptr, 0, 0}, {nullptr, 0, 0}};
         if (row < a.rows) {
-            const int slice = (int)(row / a.rows_in), r = (int)(row % a.rows_in);
+            const int slice = (int)(row / a.rows_in), r = (int)(row - (int64_t)slice * a.rows_in);
             const int b = slice / a.Hkv, kv = slice - b * a.Hkv;
             if (a.tc_splits) {
                 g[0].base = a.pre_part + ((int64_t)kv * a.prefix.rows + b * a.rows_in + r) * ps;
@@ -466,72 +478,130 @@ __global__ void __launch_bounds__(kFinThreads) serve_finish_kernel(FinishArgs a)
             }
             g[1] = parts_of(a.own, a.own_part, slice, r, ps);
         }
-        float N, L;
-        joint(g, lane, &N, &L);
-        const float inv = L != 0.f ? 1.f / L : 0.f;
+        // the prefix's partials, then the own ones, as one list; this warp's half of it
+        const int all = g[0].n + g[1].n, mid = (all + 1) / 2, p0 = half ? mid : 0, p1 = half ? all : mid;
         for (int j0 = 0; j0 < d; j0 += 128) {
-            const int j = j0 + 4 * lane;
+            const int j = min(j0 + 4 * lane, d - 4);
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int k = 0; k < 2; ++k) {
-                const int mid = (g[k].n + 1) / 2, i0 = half ? mid : 0, i1 = half ? g[k].n : mid;
-                for (int c0 = i0; c0 < i1; c0 += 32) {
-                    const int cnt = min(32, i1 - c0);
-                    float sc = 0.f;
-                    if (lane < cnt) {
-                        const float h = g[k].base[(c0 + lane) * g[k].step];
-                        sc = h == -INFINITY ? 0.f : exp2f(h - N) * inv;
-                    }
-#pragma unroll 8
-                    for (int i = 0; i < cnt; ++i) {
-                        const float f = __shfl_sync(kFull, sc, i);
-                        if (j < d) {
-                            const float4 o = *(const float4 *)(g[k].base + (c0 + i) * g[k].step + 4 + j);
-                            acc.x = fmaf(f, o.x, acc.x);
-                            acc.y = fmaf(f, o.y, acc.y);
-                            acc.z = fmaf(f, o.z, acc.z);
-                            acc.w = fmaf(f, o.w, acc.w);
-                        }
+            float N = -INFINITY, L = 0.f;
+            for (int p = p0; p < p1; p += kMgParts) {
+                float2 h[kMgParts];
+                float4 o[kMgParts];
+#pragma unroll
+                for (int k = 0; k < kMgParts; ++k) {
+                    h[k] = make_float2(-INFINITY, 0.f);
+                    o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (p + k < p1) {
+                        const Parts &q = p + k < g[0].n ? g[0] : g[1];
+                        const float *at = q.base + (p + k < g[0].n ? p + k : p + k - g[0].n) * q.step;
+                        h[k] = *(const float2 *)at;
+                        o[k] = *(const float4 *)(at + 4 + j);
                     }
                 }
+                float up = N;
+#pragma unroll
+                for (int k = 0; k < kMgParts; ++k) up = fmaxf(up, h[k].x);
+                const float sc = N == -INFINITY ? 0.f : exp2f(N - up);
+                N = up;
+                L *= sc;
+                acc.x *= sc;
+                acc.y *= sc;
+                acc.z *= sc;
+                acc.w *= sc;
+#pragma unroll
+                for (int k = 0; k < kMgParts; ++k) {
+                    const float f = h[k].x == -INFINITY ? 0.f : exp2f(h[k].x - up);
+                    L = fmaf(f, h[k].y, L);
+                    acc.x = fmaf(f, o[k].x, acc.x);
+                    acc.y = fmaf(f, o[k].y, acc.y);
+                    acc.z = fmaf(f, o[k].z, acc.z);
+                    acc.w = fmaf(f, o[k].w, acc.w);
+                }
             }
-            if (j < d) {
-                float *o = osm + (half * d + j) * kMgRows + r4;
+            if (j0 + 4 * lane < d) {
+                float *o = osm + (half * d + j) * kMgRows + r8;
                 o[0] = acc.x;
                 o[kMgRows] = acc.y;
                 o[2 * kMgRows] = acc.z;
                 o[3 * kMgRows] = acc.w;
             }
+            if (j0 == 0 && lane == 0) head[half][r8] = make_float2(N, L);
         }
     }
     __syncthreads();
-    float acc[kMgRows] = {};
-    const float4 *o0 = (const float4 *)osm + q4 * part, *o1 = o0 + d;
-    auto add = [&](float v, int k) {
-        const float4 x = o0[k], y = o1[k];
-        acc[0] = fmaf(v, x.x + y.x, acc[0]);
-        acc[1] = fmaf(v, x.y + y.y, acc[1]);
-        acc[2] = fmaf(v, x.z + y.z, acc[2]);
-        acc[3] = fmaf(v, x.w + y.w, acc[3]);
-    };
-#pragma unroll
-    for (int k = 0; k < 32; ++k)
-        if (k < part) add(first[k], k);
-    if (oc < d)
-#pragma unroll 16
-        for (int k = 32; k < part; ++k) add(w[(int64_t)k * d], k);
-#pragma unroll
-    for (int r = 0; r < kMgRows; ++r) red[q4][r][tid & 63] = acc[r];
+    // the halves of a row together, over the normaliser
+    for (int e = tid; e < d * kMgRows; e += kFinThreads) {
+        const int r = e % kMgRows;
+        const float2 x = head[0][r], y = head[1][r];
+        const float N = fmaxf(x.x, y.x);
+        const float fx = x.x == -INFINITY ? 0.f : exp2f(x.x - N), fy = y.x == -INFINITY ? 0.f : exp2f(y.x - N);
+        const float L = fx * x.y + fy * y.y, inv = L != 0.f ? 1.f / L : 0.f;
+        osm[e] = (fx * osm[e] + fy * osm[d * kMgRows + e]) * inv;
+    }
     __syncthreads();
-    const int r = tid >> 6;
-    if (row0 + r >= a.rows || oc >= d) return;
-    const float v = (red[0][r][tid & 63] + red[1][r][tid & 63]) + (red[2][r][tid & 63] + red[3][r][tid & 63]);
-    const int64_t at = (row0 + r) * d + oc;
-    if (a.dtype == TQ_F16) ((__half *)a.out)[at] = __float2half_rn(v);
-    else if (a.dtype == TQ_BF16) ((__nv_bfloat16 *)a.out)[at] = __float2bfloat16_rn(v);
-    else ((float *)a.out)[at] = v;
+    for (int c = col; c < d; c += ncol) {  // one column a thread up to d = 512
+        float acc[kMgRows] = {};
+        const float4 *o4 = (const float4 *)(osm + i0 * kMgRows);
+        auto add = [&](float v, int k) {
+            const float4 x = o4[2 * k], y = o4[2 * k + 1];
+            acc[0] = fmaf(v, x.x, acc[0]);
+            acc[1] = fmaf(v, x.y, acc[1]);
+            acc[2] = fmaf(v, x.z, acc[2]);
+            acc[3] = fmaf(v, x.w, acc[3]);
+            acc[4] = fmaf(v, y.x, acc[4]);
+            acc[5] = fmaf(v, y.y, acc[5]);
+            acc[6] = fmaf(v, y.z, acc[6]);
+            acc[7] = fmaf(v, y.w, acc[7]);
+        };
+        if (c == col) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+                if (k < part) add(first[k], k);
+        }
+#pragma unroll 16
+        for (int k = c == col ? 32 : 0; k < part; ++k) add(a.P.R[(int64_t)(i0 + k) * d + c], k);
+#pragma unroll
+        for (int r = 0; r < kMgRows; ++r) red[(tid / ncol * kMgRows + r) * ncol + col] = acc[r];
+        __syncthreads();
+        for (int e = tid; e < kMgRows * ncol; e += kFinThreads) {
+            const int r = e / ncol, cc = e - r * ncol;
+            float v = 0.f;
+            for (int k = 0; k < ks; ++k) v += red[(k * kMgRows + r) * ncol + cc];
+            if (row0 + r < a.rows) {
+                const int64_t at = (row0 + r) * d + (c - col) + cc;
+                if (a.dtype == TQ_F16) ((__half *)a.out)[at] = __float2half_rn(v);
+                else if (a.dtype == TQ_BF16) ((__nv_bfloat16 *)a.out)[at] = __float2bfloat16_rn(v);
+                else ((float *)a.out)[at] = v;
+            }
+        }
+        __syncthreads();
+    }
 }
 
 }  // namespace
+
+cudaError_t allow_smem(const void *kernel, size_t bytes) {
+    // kernels seen on each device, in a table of their own addresses; entries only ever appear
+    constexpr int kSlots = 128, kDevices = 16;
+    static std::atomic<const void *> seen[kDevices][kSlots];
+    int dev = -1;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const bool listed = dev >= 0 && dev < kDevices;
+    size_t at = ((uintptr_t)kernel >> 4) % kSlots;
+    for (int i = 0; listed && i < kSlots; ++i, at = (at + 1) % kSlots) {
+        const void *k = seen[dev][at].load(std::memory_order_acquire);
+        if (k == kernel) return cudaSuccess;
+        if (!k) break;
+    }
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e != cudaSuccess || !listed) return e;
+    for (int i = 0; i < kSlots; ++i, at = (at + 1) % kSlots) {
+        const void *none = nullptr;
+        if (seen[dev][at].compare_exchange_strong(none, kernel) || none == kernel) break;
+    }
+    return cudaSuccess;
+}
 
 cudaError_t launch_ragged_plain(const RaggedArgs &a, cudaStream_t s) {
     const size_t smem = sizeof(float) * ((size_t)(a.P.d + a.P.m) * kPlRows + kPlRows * kPlTile);
@@ -542,10 +612,10 @@ cudaError_t launch_ragged_plain(const RaggedArgs &a, cudaStream_t s) {
 
 namespace ragged {
 template <int D>
-cudaError_t launch_dim(const RaggedArgs &a, bool f32, int row_block, cudaStream_t s);
-extern template cudaError_t launch_dim<64>(const RaggedArgs &, bool, int, cudaStream_t);
-extern template cudaError_t launch_dim<128>(const RaggedArgs &, bool, int, cudaStream_t);
-extern template cudaError_t launch_dim<256>(const RaggedArgs &, bool, int, cudaStream_t);
+cudaError_t launch_dim(const RaggedPair &a, bool f32, int row_block, cudaStream_t s);
+extern template cudaError_t launch_dim<64>(const RaggedPair &, bool, int, cudaStream_t);
+extern template cudaError_t launch_dim<128>(const RaggedPair &, bool, int, cudaStream_t);
+extern template cudaError_t launch_dim<256>(const RaggedPair &, bool, int, cudaStream_t);
 }  // namespace ragged
 
 bool ragged_mma_supported(const Prepared &P) {
@@ -561,11 +631,18 @@ int ragged_mma_rows(const Prepared &P, bool f32, int64_t rows) {
 
 int ragged_mma_ctas_per_sm(const Prepared &P) { return P.d >= 256 ? 3 : 4; }
 
-cudaError_t launch_ragged_mma(const RaggedArgs &a, bool f32, int row_block, cudaStream_t s) {
-    switch (a.P.d) {
-        case 64: return ragged::launch_dim<64>(a, f32, row_block, s);
-        case 128: return ragged::launch_dim<128>(a, f32, row_block, s);
-        case 256: return ragged::launch_dim<256>(a, f32, row_block, s);
+cudaError_t launch_ragged_mma(const RaggedArgs &own, const RaggedArgs &prefix, const ServePlan &plan, bool f32,
+                              cudaStream_t s) {
+    RaggedPair p;
+    p.a[0] = own;
+    p.a[1] = prefix;
+    auto blocks = [&](const RaggedCache &c) { return (c.rows + plan.row_block - 1) / plan.row_block; };
+    p.first = plan.own_ctas ? plan.own_ctas * blocks(own.c) : 0;
+    p.total = p.first + (plan.prefix_ctas ? plan.prefix_ctas * blocks(prefix.c) : 0);
+    switch (own.P.d) {
+        case 64: return ragged::launch_dim<64>(p, f32, plan.row_block, s);
+        case 128: return ragged::launch_dim<128>(p, f32, plan.row_block, s);
+        case 256: return ragged::launch_dim<256>(p, f32, plan.row_block, s);
         default: return cudaErrorInvalidValue;
     }
 }
@@ -575,7 +652,7 @@ namespace {
 // the row blocks, and no more than there are fours of stages (a CTA's warps take one each).
 int division(int64_t slices, int64_t cap, int64_t row_blocks, int per_sm) {
     const int64_t most = slices * ((cap + 4 * kStage - 1) / (4 * kStage));
-    int64_t want = (148ll * per_sm + row_blocks - 1) / row_blocks;
+    int64_t want = ((int64_t)kSms * per_sm + row_blocks - 1) / row_blocks;
     if (want > most) want = most;
     return (int)(want < 1 ? 1 : want);
 }
@@ -590,18 +667,15 @@ ServePlan plan_serve(const Prepared &P, tq_dtype dtype, int B, int Hq, int Hkv, 
     const bool f32 = dtype == TQ_F32;
     p.fast = ragged_mma_supported(P);
     p.row_block = kPlRows;
-    p.prefix_block = kPlRows;
     const int per_sm = p.fast ? ragged_mma_ctas_per_sm(P) : 4;
-    if (p.fast) {
-        p.row_block = ragged_mma_rows(P, f32, R);
-        p.prefix_block = ragged_mma_rows(P, f32, (int64_t)B * R);
-    }
-    if (t_cap > 0) p.own_ctas = division((int64_t)B * Hkv, t_cap, (R + p.row_block - 1) / p.row_block, per_sm);
     // many 16-bit rows on one prefix: the many-row kernel
     const bool tc = p.fast && !f32 && t_prefix > 0 && (int64_t)B * R > 8;
+    // the ragged kernel takes both caches in one launch, in blocks of the larger number of rows
+    if (p.fast) p.row_block = ragged_mma_rows(P, f32, t_prefix > 0 && !tc ? (int64_t)B * R : R);
+    if (t_cap > 0) p.own_ctas = division((int64_t)B * Hkv, t_cap, (R + p.row_block - 1) / p.row_block, per_sm);
     if (tc) p.tc = prefix_split(P.d, Hkv, (int64_t)B * R, t_prefix);
     else if (t_prefix > 0)
-        p.prefix_ctas = division(Hkv, t_prefix, ((int64_t)B * R + p.prefix_block - 1) / p.prefix_block, per_sm);
+        p.prefix_ctas = division(Hkv, t_prefix, ((int64_t)B * R + p.row_block - 1) / p.row_block, per_sm);
     size_t o = 0;
     auto take = [&](size_t bytes) {
         const size_t at = o;
@@ -616,7 +690,7 @@ ServePlan plan_serve(const Prepared &P, tq_dtype dtype, int B, int Hq, int Hkv, 
         return (size_t)(slices * ((r + block - 1) / block) * block * n * 4);
     };
     p.own_frag = take(p.fast && t_cap > 0 ? frag_bytes((int64_t)B * Hkv, R, p.row_block) : 0);
-    p.pre_frag = take(p.fast && p.prefix_ctas ? frag_bytes(Hkv, (int64_t)B * R, p.prefix_block) : 0);
+    p.pre_frag = take(p.fast && p.prefix_ctas ? frag_bytes(Hkv, (int64_t)B * R, p.row_block) : 0);
     p.qrows = take(tc ? sizeof(uint16_t) * (size_t)(rows * n) : 0);
     p.fscale = take(sizeof(float) * (size_t)rows);
     p.zbuf = take(weigh ? sizeof(float) * (size_t)rows * (size_t)t_cap : 0);
@@ -647,8 +721,7 @@ cudaError_t launch_serve(const ServeCall &call, const ServePlan &plan, void *scr
     if (plan.fast && plan.prefix_ctas) pa.pre_frag = (uint16_t *)(base + plan.pre_frag);
     if (plan.tc.splits) pa.qrows = (uint16_t *)(base + plan.qrows);
     pa.row_block = plan.row_block;
-    pa.prefix_block = plan.prefix_block;
-    pa.prefix_blocks = (int)(((int64_t)call.B * R + plan.prefix_block - 1) / plan.prefix_block);
+    pa.prefix_blocks = (int)(((int64_t)call.B * R + plan.row_block - 1) / plan.row_block);
     pa.lens = call.lens;
     pa.B = call.B;
     pa.t_cap = call.t_cap;
@@ -680,7 +753,7 @@ cudaError_t launch_serve(const ServeCall &call, const ServePlan &plan, void *scr
         own.c.ctas = plan.own_ctas;
         own.part = (float *)(base + plan.own_part);
         own.zbuf = call.weights ? (float *)(base + plan.zbuf) : nullptr;
-        e = plan.fast ? launch_ragged_mma(own, call.dtype == TQ_F32, plan.row_block, s) : launch_ragged_plain(own, s);
+        if (!plan.fast) e = launch_ragged_plain(own, s);
         if (e != cudaSuccess) return e;
     }
     if (call.t_prefix > 0) {
@@ -694,9 +767,12 @@ cudaError_t launch_serve(const ServeCall &call, const ServePlan &plan, void *scr
         pre.c.rows_outer = (int64_t)call.Hkv * R;
         pre.c.ctas = plan.prefix_ctas;
         pre.part = (float *)(base + plan.pre_part);
-        e = plan.tc.splits ? launch_prefix_tc(P, pre.c, pa.qrows, pa.fscale, pre.part, plan.tc, call.dev_status, s)
-            : plan.fast    ? launch_ragged_mma(pre, call.dtype == TQ_F32, plan.prefix_block, s)
-                           : launch_ragged_plain(pre, s);
+        if (plan.tc.splits) e = launch_prefix_tc(P, pre.c, pa.qrows, pa.fscale, pre.part, plan.tc, call.dev_status, s);
+        else if (!plan.fast) e = launch_ragged_plain(pre, s);
+        if (e != cudaSuccess) return e;
+    }
+    if (plan.fast && (plan.own_ctas || plan.prefix_ctas)) {
+        e = launch_ragged_mma(own, pre, plan, call.dtype == TQ_F32, s);
         if (e != cudaSuccess) return e;
     }
     FinishArgs fa;
@@ -712,7 +788,7 @@ cudaError_t launch_serve(const ServeCall &call, const ServePlan &plan, void *scr
     fa.Hkv = call.Hkv;
     fa.dtype = call.dtype;
     fa.out = call.out;
-    const int64_t merge = (call.rows + kMgRows - 1) / kMgRows * ((P.d + kMgCols - 1) / kMgCols);
+    const int64_t merge = (call.rows + kMgRows - 1) / kMgRows;
     int64_t weigh = 0;
     if (call.weights) {
         fa.zbuf = own.zbuf;
@@ -721,7 +797,18 @@ cudaError_t launch_serve(const ServeCall &call, const ServePlan &plan, void *scr
         weigh = (int64_t)fa.chunks * call.B * call.Hkv;
     }
     fa.merge_ctas = (unsigned)merge;
-    serve_finish_kernel<<<(unsigned)(merge + weigh), kFinThreads, 2 * sizeof(float) * kMgRows * P.d, s>>>(fa);
+    const size_t fin_smem = 2 * sizeof(float) * kMgRows * P.d;
+    if (fin_smem >= 32 * 1024) {  // with the static arrays above what is allowed without asking
+        e = allow_smem((const void *)serve_finish_kernel, 2 * sizeof(float) * kMgRows * kMaxDim);
+        if (e != cudaSuccess) return e;
+    }
+    // Few weighing CTAs ride along with the merging ones; many get a launch of their own, where more of
+    // them fit an SM (8 against 1: 11 against 50 us for 2048 of them).
+    const bool along = weigh <= kSms;
+    serve_finish_kernel<<<(unsigned)(merge + (along ? weigh : 0)), kFinThreads, fin_smem, s>>>(fa);
+    e = cudaGetLastError();
+    if (e != cudaSuccess || along) return e;
+    serve_weigh_kernel<<<(unsigned)weigh, kWtThreads, 0, s>>>(fa);
     return cudaGetLastError();
 }
 

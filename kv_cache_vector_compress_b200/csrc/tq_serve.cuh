@@ -22,6 +22,7 @@
 
 namespace tq {
 
+constexpr int kSms = 148;     // grid sizing (fixed so that scratch sizes do not vary)
 constexpr int kStage = 32;       // tokens of one copy stage: the unit in which contexts are divided
 constexpr float kMinNorm = 5.9604644775390625e-8f;  // 2^-24
 constexpr float kLog2eF = 1.4426950408889634f;
@@ -66,13 +67,15 @@ __device__ __forceinline__ int64_t cta_first(int64_t total, int ctas, int i) {
     return i >= g ? total : total * i / g;
 }
 
-// The piece that starts at stage w (< w1) of the division.
+// The piece that starts at stage w (< w1) of the division.  Called by whole warps.
 __device__ __forceinline__ Piece piece_at(const RaggedCache &c, int64_t w, int64_t w1) {
-    int lo = 0, hi = c.nseq - 1;  // the last sequence whose first stage is <= w and that has stages
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (c.cum[mid] * c.per_seq <= w) lo = mid;
-        else hi = mid - 1;
+    // the last sequence whose first stage is <= w: it has stages (all lanes of a warp look together)
+    int lo = -1;
+    for (int b0 = 0; b0 < c.nseq; b0 += 32) {
+        const int b = b0 + (int)(threadIdx.x & 31);
+        const int before = __popc(__ballot_sync(kFull, b < c.nseq && c.cum[b] * c.per_seq <= w));
+        lo += before;
+        if (before < 32) break;
     }
     const int64_t base = c.cum[lo] * c.per_seq, n = c.cum[lo + 1] - c.cum[lo];
     const int64_t h = (w - base) / n;
@@ -175,8 +178,7 @@ struct ServeCall {
 // How a call is computed: by sizes alone, so that the scratch size follows from them too.
 struct ServePlan {
     bool fast;         // the tensor-core kernels (else the plain kernel)
-    int row_block;     // query rows a CTA of the ragged kernel takes, own caches
-    int prefix_block;  // ... and the prefix
+    int row_block;     // query rows a CTA of the ragged kernel takes
     int own_ctas;      // division of the own caches (0: no own caches)
     int prefix_ctas;   // division of the prefix by the ragged kernel (0: not by it)
     PrefixSplit tc;    // splits of the prefix by the many-row kernel (0: not by it)
@@ -202,6 +204,14 @@ cudaError_t launch_ragged_plain(const RaggedArgs &a, cudaStream_t s);
 bool ragged_mma_supported(const Prepared &P);
 int ragged_mma_rows(const Prepared &P, bool f32, int64_t rows);  // the row block for so many rows a slice
 int ragged_mma_ctas_per_sm(const Prepared &P);
-cudaError_t launch_ragged_mma(const RaggedArgs &a, bool f32, int row_block, cudaStream_t s);
+// One launch for the own caches and the prefix (those that the plan gives CTAs).
+struct RaggedPair {
+    RaggedArgs a[2];
+    int first, total;  // CTAs of a[0], and of both; CTA i of a cache: division i % ctas, row block i / ctas
+};
+cudaError_t launch_ragged_mma(const RaggedArgs &own, const RaggedArgs &prefix, const ServePlan &plan, bool f32,
+                              cudaStream_t s);
+// cudaFuncSetAttribute for a kernel's dynamic shared memory, once for each kernel and device.
+cudaError_t allow_smem(const void *kernel, size_t bytes);
 
 }  // namespace tq

@@ -415,39 +415,56 @@ def _row_dtype(dtype: torch.dtype) -> int:
     return _ROW_DTYPES[dtype]
 
 
-def _need(t, name: str, dtype: torch.dtype, n: int, dev: torch.device):
-    """Raise unless t is a tensor of dtype with n values on the device of the other tensors."""
-    if t.dtype != dtype:
+def _arg(t, name: str, dtype: torch.dtype, n: int, dev: int) -> int:
+    """The address of t, a contiguous tensor of n values of dtype on CUDA device dev."""
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}")
     if t.numel() != n:
         raise ValueError(f"{name} must hold {n} values, not {t.numel()}")
-    if t.device != dev:
-        raise ValueError(f"{name} must be on {dev}")
+    if not t.is_cuda or t.get_device() != dev:
+        raise ValueError(f"{name} must be on CUDA device {dev}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
-def _on_current(p: Params, dev: torch.device):
-    if dev.type != "cuda" or dev.index != torch.cuda.current_device() or p.workspace.device != dev:
+def _device(p: Params, t: torch.Tensor) -> int:
+    """The current device, which must be that of t and of the parameter set."""
+    dev = torch.cuda.current_device()
+    if not t.is_cuda or t.get_device() != dev or p.workspace.get_device() != dev:
         raise ValueError("the tensors and the parameter set must be on the current CUDA device")
+    return dev
 
 
-def _need_cache(p: Params, keys, values, n: int, what: str, dev: torch.device):
-    """Check a cache of n records (keys: codes, signs, norm, rnorm; values: codes, norm)."""
+def _cache_args(p: Params, keys, values, n: int, what: str, dev: int):
+    """The addresses of a cache of n records (keys: codes, signs, norm, rnorm; values: codes, norm)."""
     kc, ks, kn, kr = keys
     vc, vn = values
-    _need(kc, f"{what} key codes", torch.int32, n * p.key_words(), dev)
-    _need(ks, f"{what} key signs", torch.int32, n * (p.proj_dim // 32), dev)
-    _need(kn, f"{what} key norms", torch.float16, n, dev)
-    _need(kr, f"{what} key residual norms", torch.float16, n, dev)
-    _need(vc, f"{what} value codes", torch.int32, n * p.value_words(), dev)
-    _need(vn, f"{what} value norms", torch.float16, n, dev)
+    i32, f16 = torch.int32, torch.float16
+    return (_arg(kc, f"{what} key codes", i32, n * p.key_words(), dev),
+            _arg(ks, f"{what} key signs", i32, n * (p.proj_dim // 32), dev), _arg(kn, f"{what} key norms", f16, n, dev),
+            _arg(kr, f"{what} key residual norms", f16, n, dev),
+            _arg(vc, f"{what} value codes", i32, n * p.value_words(), dev),
+            _arg(vn, f"{what} value norms", f16, n, dev))
 
 
-def _need_rest(p: Params, q, out, scratch, need: int, dev_status):
-    _need(out, "out", q.dtype, q.numel(), q.device)
-    if scratch.device != q.device or scratch.numel() * scratch.element_size() < need:
-        raise ValueError(f"scratch must hold {need} bytes on {q.device}")
-    if dev_status is not None:
-        _need(dev_status, "dev_status", torch.int32, 1, q.device)
+def _scratch_arg(scratch, need, dev: int):
+    """(address, bytes) of the caller's scratch, or of a new one of need() bytes kept in the last place."""
+    if scratch is None:
+        scratch = torch.empty(max(need(), 16), dtype=torch.uint8, device=dev)
+    elif not scratch.is_cuda or scratch.get_device() != dev:
+        raise ValueError(f"scratch must be on CUDA device {dev}")
+    elif not scratch.is_contiguous():
+        raise ValueError("scratch must be contiguous")
+    return scratch.data_ptr(), scratch.numel() * scratch.element_size(), scratch
+
+
+def _status_arg(dev_status, dev: int):
+    return None if dev_status is None else _arg(dev_status, "dev_status", torch.int32, 1, dev)
+
+
+def _raw_stream(dev: int) -> int:
+    return torch.cuda.current_stream(dev).cuda_stream
 
 
 def tq_attend_shared_scratch_bytes(p: Params, dtype: torch.dtype, B, Hq, Hkv, Nq, t_prefix, t_cap) -> int:
@@ -461,26 +478,20 @@ def tq_attend_shared(p: Params, q: torch.Tensor, prefix_keys, prefix_values, key
     tokens (int32 [B]) of each sequence's own cache (records [B, Hkv, t_cap]).  The prefix tuples are
     None when t_prefix is 0; the own ones and lens when t_cap is 0."""
     B, Hq, Nq, d = q.shape
-    dt, dev = _row_dtype(q.dtype), q.device
-    _on_current(p, dev)
-    if d != p.dim:
-        raise ValueError(f"q must have {p.dim} coordinates")
-    if t_prefix > 0:
-        _need_cache(p, prefix_keys, prefix_values, Hkv * t_prefix, "prefix", dev)
-    if t_cap > 0:
-        _need_cache(p, keys, values, B * Hkv * t_cap, "own", dev)
-        _need(lens, "lens", torch.int32, B, dev)
-    need = tq_attend_shared_scratch_bytes(p, q.dtype, B, Hq, Hkv, Nq, t_prefix, t_cap)
+    dt, dev = _row_dtype(q.dtype), _device(p, q)
+    n = B * Hq * Nq * p.dim
     if out is None:
-        out = torch.empty_like(q, memory_format=torch.contiguous_format)
-    if scratch is None:
-        scratch = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
-    _need_rest(p, q, out, scratch, need, dev_status)
-    pre = [_ptr(t) for t in (*prefix_keys, *prefix_values)] if t_prefix > 0 else [None] * 6
-    own = [_ptr(t) for t in (*keys, *values)] if t_cap > 0 else [None] * 6
-    _check(_lib.tq_attend_shared(p.ref, _ptr(q), dt, B, Hq, Hkv, Nq, t_prefix, *pre, _ptr(lens if t_cap > 0 else None),
-                                 t_cap, *own, float(scale), _ptr(out), _ptr(scratch), scratch.numel() * scratch.element_size(),
-                                 _ptr(dev_status), _stream()), "tq_attend_shared")
+        out = torch.empty((B, Hq, Nq, d), dtype=q.dtype, device=q.device)
+    pre = _cache_args(p, prefix_keys, prefix_values, Hkv * t_prefix, "prefix", dev) if t_prefix > 0 else (None,) * 6
+    own, ln = (None,) * 6, None
+    if t_cap > 0:
+        own = _cache_args(p, keys, values, B * Hkv * t_cap, "own", dev)
+        ln = _arg(lens, "lens", torch.int32, B, dev)
+    sc, nb, _keep = _scratch_arg(
+        scratch, lambda: tq_attend_shared_scratch_bytes(p, q.dtype, B, Hq, Hkv, Nq, t_prefix, t_cap), dev)
+    _check(_lib.tq_attend_shared(p.ref, _arg(q, "q", q.dtype, n, dev), dt, B, Hq, Hkv, Nq, t_prefix, *pre, ln, t_cap, *own,
+                                 scale, _arg(out, "out", q.dtype, n, dev), sc, nb, _status_arg(dev_status, dev),
+                                 _raw_stream(dev)), "tq_attend_shared")
     return out
 
 
@@ -495,23 +506,18 @@ def tq_attend_weigh(p: Params, q: torch.Tensor, keys, values, lens: torch.Tensor
     place) the softmax weight every token got, summed over the query rows of its KV head.  Returns
     the output, of q's type."""
     B, Hq, Nq, d = q.shape
-    dt, dev = _row_dtype(q.dtype), q.device
-    _on_current(p, dev)
-    if d != p.dim:
-        raise ValueError(f"q must have {p.dim} coordinates")
-    _need_cache(p, keys, values, B * Hkv * t_cap, "own", dev)
-    _need(lens, "lens", torch.int32, B, dev)
-    _need(weights, "weights", torch.float32, B * Hkv * t_cap, dev)
-    need = tq_attend_weigh_scratch_bytes(p, q.dtype, B, Hq, Hkv, Nq, t_cap)
+    dt, dev = _row_dtype(q.dtype), _device(p, q)
+    n = B * Hq * Nq * p.dim
     if out is None:
-        out = torch.empty_like(q, memory_format=torch.contiguous_format)
-    if scratch is None:
-        scratch = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
-    _need_rest(p, q, out, scratch, need, dev_status)
-    _check(_lib.tq_attend_weigh(p.ref, _ptr(q), dt, B, Hq, Hkv, Nq, _ptr(lens), t_cap,
-                                *[_ptr(t) for t in (*keys, *values)], float(scale), _ptr(weights), _ptr(out),
-                                _ptr(scratch), scratch.numel() * scratch.element_size(), _ptr(dev_status), _stream()),
-           "tq_attend_weigh")
+        out = torch.empty((B, Hq, Nq, d), dtype=q.dtype, device=q.device)
+    own = _cache_args(p, keys, values, B * Hkv * t_cap, "own", dev)
+    sc, nb, _keep = _scratch_arg(
+        scratch, lambda: tq_attend_weigh_scratch_bytes(p, q.dtype, B, Hq, Hkv, Nq, t_cap), dev)
+    _check(_lib.tq_attend_weigh(p.ref, _arg(q, "q", q.dtype, n, dev), dt, B, Hq, Hkv, Nq,
+                                _arg(lens, "lens", torch.int32, B, dev), t_cap, *own, scale,
+                                _arg(weights, "weights", torch.float32, B * Hkv * t_cap, dev),
+                                _arg(out, "out", q.dtype, n, dev), sc, nb, _status_arg(dev_status, dev),
+                                _raw_stream(dev)), "tq_attend_weigh")
     return out
 
 
@@ -527,13 +533,9 @@ def tq_evict(p: Params, keys, values, weights: torch.Tensor, lens: torch.Tensor,
     (out_keys, out_values, out_weights, kept, out_lens): the destination cache, its weights
     [B, Hkv, out_cap], the kept slots int32 [B, Hkv, budget] and the new lengths int32 [B].
     Entries behind a slice's kept tokens are not written."""
-    B, dev = lens.numel(), lens.device
-    _on_current(p, dev)
+    B, dev = lens.numel(), _device(p, lens)
     n, m = B * Hkv * t_cap, B * Hkv * out_cap
-    _need_cache(p, keys, values, n, "own", dev)
-    _need(lens, "lens", torch.int32, B, dev)
-    _need(weights, "weights", torch.float32, n, dev)
-    new = lambda *shape, dtype: torch.empty(shape, dtype=dtype, device=dev)  # noqa: E731
+    new = lambda *shape, dtype: torch.empty(shape, dtype=dtype, device=lens.device)  # noqa: E731
     if out_keys is None:
         out_keys = (new(m, p.key_words(), dtype=torch.int32), new(m, p.proj_dim // 32, dtype=torch.int32),
                     new(m, dtype=torch.float16), new(m, dtype=torch.float16))
@@ -545,19 +547,12 @@ def tq_evict(p: Params, keys, values, weights: torch.Tensor, lens: torch.Tensor,
         kept = new(B, Hkv, budget, dtype=torch.int32)
     if out_lens is None:
         out_lens = new(B, dtype=torch.int32)
-    _need_cache(p, out_keys, out_values, m, "destination", dev)
-    _need(out_weights, "out_weights", torch.float32, m, dev)
-    _need(kept, "kept", torch.int32, B * Hkv * budget, dev)
-    _need(out_lens, "out_lens", torch.int32, B, dev)
-    need = tq_evict_scratch_bytes(p, B, Hkv, t_cap, budget)
-    if scratch is None:
-        scratch = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
-    if scratch.device != dev or scratch.numel() * scratch.element_size() < need:
-        raise ValueError(f"scratch must hold {need} bytes on {dev}")
-    if dev_status is not None:
-        _need(dev_status, "dev_status", torch.int32, 1, dev)
-    _check(_lib.tq_evict(p.ref, B, Hkv, _ptr(lens), t_cap, *[_ptr(t) for t in (*keys, *values)], _ptr(weights), budget,
-                         recent, out_cap, *[_ptr(t) for t in (*out_keys, *out_values)], _ptr(out_weights), _ptr(kept),
-                         _ptr(out_lens), _ptr(scratch), scratch.numel() * scratch.element_size(), _ptr(dev_status),
-                         _stream()), "tq_evict")
+    i32, f32 = torch.int32, torch.float32
+    sc, nb, _keep = _scratch_arg(scratch, lambda: tq_evict_scratch_bytes(p, B, Hkv, t_cap, budget), dev)
+    _check(_lib.tq_evict(p.ref, B, Hkv, _arg(lens, "lens", i32, B, dev), t_cap,
+                         *_cache_args(p, keys, values, n, "own", dev), _arg(weights, "weights", f32, n, dev), budget,
+                         recent, out_cap, *_cache_args(p, out_keys, out_values, m, "destination", dev),
+                         _arg(out_weights, "out_weights", f32, m, dev), _arg(kept, "kept", i32, B * Hkv * budget, dev),
+                         _arg(out_lens, "out_lens", i32, B, dev), sc, nb, _status_arg(dev_status, dev),
+                         _raw_stream(dev)), "tq_evict")
     return out_keys, out_values, out_weights, kept, out_lens

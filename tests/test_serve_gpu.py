@@ -421,7 +421,7 @@ def test_binding_checks(tq):
         tq.tq_attend_weigh(pr.p, pr.q[..., :64], pr.k, pr.v, pr.dlens, 2, 20, w)
     with pytest.raises(ValueError):
         tq.tq_attend_weigh(pr.p, pr.q, pr.k, pr.v, pr.dlens.cpu(), 2, 20, w)
-    with pytest.raises(ValueError):
+    with pytest.raises(tq.TQError):
         tq.tq_attend_weigh(pr.p, pr.q, pr.k, pr.v, pr.dlens, 2, 20, w, scratch=w[:1, :1, :1])
     with pytest.raises(ValueError):
         tq.tq_attend_weigh(pr.p, pr.q.repeat(1, 1, 2, 1).transpose(1, 2).contiguous().transpose(1, 2), pr.k, pr.v,
