@@ -9,6 +9,7 @@
 // each from a histogram of the keys that match the digits before.
 #include "tq_common.cuh"
 #include "tq_evict.cuh"
+#include "tq_launch.cuh"
 
 namespace tq {
 
@@ -24,6 +25,18 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
     return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
+// This warp's exclusive prefix of the warps' sums, and their total.
+__device__ __forceinline__ uint32_t before_warp(const uint32_t *wsum, int warp, int lane, uint32_t *all) {
+    const uint32_t v = wsum[lane];
+    uint32_t s = v;
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t y = __shfl_up_sync(kFull, s, o);
+        if (lane >= o) s += y;
+    }
+    *all = __shfl_sync(kFull, s, 31);
+    return __shfl_sync(kFull, s - v, warp);
+}
+
 // One CTA per slice; a thread holds up to KPT keys in registers, loaded at once, so that the slice is
 // read once while it has at most KPT x 1024 tokens (longer ones in rounds, read again from L2 by each
 // step).  Three histograms in shared memory find the threshold; then every warp's counts of each group of 32
@@ -31,6 +44,7 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 template <int KPT>
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictCall c) {
     constexpr int ROUND = KPT * kSelThreads;
+    grid_go();
     __shared__ uint32_t hist[kBins];
     __shared__ uint32_t cnt[KPT * kSelWarps];  // [group of a round][warp]: keys above | keys equal << 16
     __shared__ uint32_t wsum[kSelWarps];
@@ -92,8 +106,8 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictCall c) 
         }
         if (lane == 31) wsum[warp] = x;
         __syncthreads();
-        uint32_t above = x - (h1 + h0);
-        for (int u = 0; u < warp; ++u) above += wsum[u];
+        uint32_t all;
+        const uint32_t above = x - (h1 + h0) + before_warp(wsum, warp, lane, &all);
         if (above < rank && rank <= above + h1) {
             s_digit = (uint32_t)hi;
             s_rank = rank - above;
@@ -131,12 +145,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictCall c) 
             }
             if (lane == 31) wsum[warp] = s;
             __syncthreads();
-            uint32_t off = 0;
-            for (int u = 0; u < kSelWarps; ++u) {
-                const uint32_t v = wsum[u];
-                if (u < warp) off += v;
-                all += v;
-            }
+            const uint32_t off = before_warp(wsum, warp, lane, &all);
             if (tid < KPT * kSelWarps) cnt[tid] = off + s - x;
         }
         __syncthreads();
@@ -192,6 +201,7 @@ __device__ __forceinline__ void copy_wide(const EvictCall &c, int a, int64_t src
 __global__ void __launch_bounds__(kCopyThreads) evict_copy_kernel(EvictCall c, int chunks) {
     static_assert(kCopySlots == kCopyThreads, "a thread a record");
     __shared__ int32_t idx[kCopySlots];
+    grid_wait();
     const int slice = blockIdx.x / chunks, tid = threadIdx.x;
     const int j0 = (blockIdx.x - slice * chunks) * kCopySlots;
     const int cnt = min(kCopySlots, c.counts[slice] - j0);
@@ -231,8 +241,7 @@ cudaError_t launch_evict(const EvictCall &c, cudaStream_t s) {
                                                         : launch_select<32>(c, s);
     if (e != cudaSuccess) return e;
     const int chunks = (int)evict_chunks(c.budget);
-    evict_copy_kernel<<<(unsigned)(chunks * c.B * c.Hkv), kCopyThreads, 0, s>>>(c, chunks);
-    return cudaGetLastError();
+    return launch_after(evict_copy_kernel, (unsigned)(chunks * c.B * c.Hkv), kCopyThreads, 0, s, c, chunks);
 }
 
 }  // namespace tq

@@ -37,6 +37,7 @@
 #include <type_traits>
 
 #include "tq_decode.cuh"
+#include "tq_launch.cuh"
 #include "tq_serve.cuh"
 #include "tq_sm100.cuh"
 
@@ -239,7 +240,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(PrefixArgs a) {
     uint32_t *tmem_s = (uint32_t *)(sm + C::OB + 16 * 8 + 8);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-    const int kv = blockIdx.x / a.splits, split = blockIdx.x - kv * a.splits, rt = blockIdx.y;
+    const int unit = blockIdx.x / a.splits, split = blockIdx.x - unit * a.splits, kv = unit % a.c.slices,
+              rt = unit / a.c.slices;
     const int T = (int)a.c.stride, tiles = (T - 1) / TT + 1;
     const int j0 = split * a.tiles_per, nT = min(a.tiles_per, tiles - j0);
 
@@ -275,6 +277,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(PrefixArgs a) {
         float *xch = (float *)(sm + C::OX);
         volatile int *flags = (volatile int *)(sm + C::OX + 2 * 128 * 4);  // [two tiles, gave up][half][quarter]
         auto pair_sync = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory"); };
+        grid_wait();  // the preparation's rows; nothing else here is written by the kernel before
+        if (tid == 0) grid_go();
         {  // the query rows into tensor memory
             const uint4 *q = (const uint4 *)(a.qrows + ((int64_t)kv * a.c.rows + row) * C::K);
 #pragma unroll 2
@@ -648,9 +652,7 @@ cudaError_t launch_one(const PrefixArgs &a, int row_tiles, cudaStream_t s) {
     using C = Cfg<D, KB>;
     cudaError_t e = allow_smem((const void *)prefix_tc_kernel<D, KB>, C::SMEM);
     if (e != cudaSuccess) return e;
-    dim3 grid((unsigned)(a.splits * a.c.slices), (unsigned)row_tiles);
-    prefix_tc_kernel<D, KB><<<grid, kThreads, C::SMEM, s>>>(a);
-    return cudaGetLastError();
+    return launch_after(prefix_tc_kernel<D, KB>, (unsigned)(a.splits * a.c.slices * row_tiles), kThreads, C::SMEM, s, a);
 }
 
 template <int D>

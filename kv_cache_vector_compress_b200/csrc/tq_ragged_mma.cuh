@@ -19,6 +19,7 @@
 #include <float.h>
 
 #include "tq_decode.cuh"
+#include "tq_launch.cuh"
 #include "tq_serve.cuh"
 
 namespace tq {
@@ -95,6 +96,10 @@ __global__ void __launch_bounds__(NW * 32, D >= 256 ? 3 : F32 || NT > 1 ? 3 : 4)
     constexpr int VB = C::VB, VN = VB < 3 ? VB : 3;
     extern __shared__ __align__(16) uint8_t smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gid = lane >> 2, t4 = lane & 3;
+    // Behind the many-row prefix kernel this one runs beside it: that kernel lets it start when its own
+    // wait for the preparation is over, and the wait at the end makes the merge wait for both.
+    grid_go();
+    if (!pair.late_wait) grid_wait();
     const bool second = (int)blockIdx.x >= pair.first;
     const RaggedArgs &a = pair.a[second];
     const int id = (int)blockIdx.x - (second ? pair.first : 0), cta = id % a.c.ctas, rblk = id / a.c.ctas;
@@ -102,7 +107,10 @@ __global__ void __launch_bounds__(NW * 32, D >= 256 ? 3 : F32 || NT > 1 ? 3 : 4)
     const int64_t total = ragged_total(a.c);
     const int64_t w1 = cta_first(total, a.c.ctas, cta + 1);
     int64_t w = cta_first(total, a.c.ctas, cta);
-    if (w >= w1) return;
+    if (w >= w1) {
+        grid_wait();
+        return;
+    }
     const int r0 = rblk * C::ROWS, nr = min(C::ROWS, a.c.rows - r0);
     const ServeTables *T = a.P.serve;
     const Lut kh = load_lut<(1 << KB)>(T->kh);
@@ -461,6 +469,7 @@ __global__ void __launch_bounds__(NW * 32, D >= 256 ? 3 : F32 || NT > 1 ? 3 : 4)
             }
         }
     }
+    grid_wait();
 }
 
 template <int D, int KB, int NT, bool F32>
@@ -468,8 +477,7 @@ cudaError_t launch_one(const RaggedPair &a, cudaStream_t s) {
     using C = Cfg<D, KB, NT, F32>;
     cudaError_t e = allow_smem((const void *)ragged_mma_kernel<D, KB, NT, F32>, C::SMEM);
     if (e != cudaSuccess) return e;
-    ragged_mma_kernel<D, KB, NT, F32><<<(unsigned)a.total, NW * 32, C::SMEM, s>>>(a);
-    return cudaGetLastError();
+    return launch_after(ragged_mma_kernel<D, KB, NT, F32>, (unsigned)a.total, NW * 32, C::SMEM, s, a);
 }
 
 // The instances of one head dimension; defined in tq_ragged_<D>.cu.

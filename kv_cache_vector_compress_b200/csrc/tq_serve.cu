@@ -8,6 +8,7 @@
 
 #include <cuda_bf16.h>
 
+#include "tq_launch.cuh"
 #include "tq_serve.cuh"
 
 namespace tq {
@@ -47,14 +48,17 @@ __device__ __forceinline__ float load_elem(const void *p, tq_dtype t, int64_t i)
     return ((const float *)p)[i];
 }
 
-// Sum over this thread's quarter of the coordinates j of w[j ld] x[j][0..7], CH loads in flight.
+// Sum over this thread's quarter of the coordinates j of w[j ld] x[j][0..7]: the first of w's loads
+// are in v already, the others go CH at a time.
+constexpr int kPrepFirst = 32;
 template <int CH>
-__device__ __forceinline__ void quarter_dot(const float *w, int64_t ld, const float *x, int count,
-                                            float (&acc)[kPrepRows]) {
+__device__ __forceinline__ void quarter_dot(float (&v)[kPrepFirst], const float *w, int64_t ld, const float *x,
+                                            int count, float (&acc)[kPrepRows]) {
     for (int j0 = 0; j0 < count; j0 += CH) {
-        float v[CH];
+        if (j0 > 0) {
 #pragma unroll
-        for (int k = 0; k < CH; ++k) v[k] = w[(j0 + k) * ld];
+            for (int k = 0; k < CH; ++k) v[k] = w[(j0 + k) * ld];
+        }
 #pragma unroll
         for (int k = 0; k < CH; ++k) {
             const float4 a = *(const float4 *)(x + (j0 + k) * kPrepRows), b = *(const float4 *)(x + (j0 + k) * kPrepRows + 4);
@@ -86,7 +90,8 @@ __device__ __forceinline__ void put_frag(uint16_t *frag, int64_t slice, int bloc
 // A CTA computes kPrepCols operands of kPrepRows rows: latency bound at a few rows (three dependent
 // steps: the rows, the loads of R^T in flight together, the exchange of the quarters), and at many
 // by its reads of R^T and S^T from L2.  The last CTA lays out the contexts instead.
-__global__ void __launch_bounds__(kPrepThreads) serve_prep_kernel(PrepArgs a) {
+__global__ void __launch_bounds__(kPrepThreads, 3) serve_prep_kernel(PrepArgs a) {
+    grid_go();
     extern __shared__ __align__(16) float qT[];  // [d][kPrepRows]
     __shared__ float red[4][kPrepRows][kPrepCols];
     __shared__ float rmax[kPrepRows];
@@ -137,27 +142,30 @@ __global__ void __launch_bounds__(kPrepThreads) serve_prep_kernel(PrepArgs a) {
     const int64_t r0 = (int64_t)(blockIdx.x / cols) * kPrepRows;
     const int nr = (int)min((int64_t)kPrepRows, a.rows - r0);
     const int cb = (blockIdx.x % cols) * kPrepCols;
+    // this thread's operand c and quarter of the sum; the loads that need no row first
+    const int c = cb + (tid & 63), q4 = tid >> 6, part = d >> 2;
+    const int64_t ld = c < d ? d : m;
+    const float *w = (c < d ? P.RT + c : P.ST + (c - d)) + q4 * part * ld;
+    float v[kPrepFirst];
+#pragma unroll
+    for (int k = 0; k < kPrepFirst; ++k) v[k] = c < n && k < part ? w[k * ld] : 0.f;
     {  // a warp a row
         float mx = 0.f;
         for (int j = lane; j < d; j += 32) {
-            const float v = warp < nr ? load_elem(a.q, a.dtype, (r0 + warp) * d + j) : 0.f;
-            qT[j * kPrepRows + warp] = v;
-            mx = fmaxf(mx, fabsf(v));
+            const float x = warp < nr ? load_elem(a.q, a.dtype, (r0 + warp) * d + j) : 0.f;
+            qT[j * kPrepRows + warp] = x;
+            mx = fmaxf(mx, fabsf(x));
         }
         mx = warp_max(mx);
         if (lane == 0) rmax[warp] = mx;
     }
     __syncthreads();
     {
-        const int c = cb + (tid & 63), q4 = tid >> 6, part = d >> 2;
         float acc[kPrepRows] = {};
         if (c < n) {
-            const float *w = c < d ? P.RT + c : P.ST + (c - d);
-            const int64_t ld = c < d ? d : m;
-            w += q4 * part * ld;
             const float *x = qT + q4 * part * kPrepRows;
-            if (part >= 32) quarter_dot<32>(w, ld, x, part, acc);
-            else quarter_dot<8>(w, ld, x, part, acc);
+            if (part >= 32) quarter_dot<32>(v, w, ld, x, part, acc);
+            else quarter_dot<8>(v, w, ld, x, part, acc);
         }
 #pragma unroll
         for (int r = 0; r < kPrepRows; ++r) red[q4][r][tid & 63] = acc[r];
@@ -175,16 +183,16 @@ __global__ void __launch_bounds__(kPrepThreads) serve_prep_kernel(PrepArgs a) {
     for (int k = 0; k < 2; ++k) {
         const int cc = lane + 32 * k, c = cb + cc;
         if (c >= n) break;
-        const float v = ((red[0][r][cc] + red[1][r][cc]) + (red[2][r][cc] + red[3][r][cc])) *
+        const float x = ((red[0][r][cc] + red[1][r][cc]) + (red[2][r][cc] + red[3][r][cc])) *
                         ((c < d ? sigma : gamma) * down);
-        if (a.qprep) a.qprep[row * n + c] = v;
+        if (a.qprep) a.qprep[row * n + c] = x;
         if (a.own_frag)
-            put_frag(a.own_frag, slice, (a.rows_in + a.row_block - 1) / a.row_block, a.row_block, d, P.kbeta, rr, c, v);
+            put_frag(a.own_frag, slice, (a.rows_in + a.row_block - 1) / a.row_block, a.row_block, d, P.kbeta, rr, c, x);
         if (a.qrows)
             a.qrows[((int64_t)kv * a.B * a.rows_in + (int64_t)b * a.rows_in + rr) * n + prefix_column(d, c)] =
-                __half_as_ushort(__float2half_rn(v));
+                __half_as_ushort(__float2half_rn(x));
         if (a.pre_frag)
-            put_frag(a.pre_frag, kv, a.prefix_blocks, a.row_block, d, P.kbeta, b * a.rows_in + rr, c, v);
+            put_frag(a.pre_frag, kv, a.prefix_blocks, a.row_block, d, P.kbeta, b * a.rows_in + rr, c, x);
     }
 }
 
@@ -198,6 +206,8 @@ constexpr int kPlCoord = kMaxDim / kPlThreads;
 // One CTA: its pieces of the slices, for kPlRows query rows (blockIdx.y).  Scores with a thread a
 // token, online softmax, then the weighted value sum with a thread a coordinate; fp32 throughout.
 __global__ void __launch_bounds__(kPlThreads) ragged_plain_kernel(RaggedArgs a) {
+    grid_go();
+    grid_wait();
     extern __shared__ __align__(16) float sm[];  // qs[(d + m)][kPlRows], ps[kPlRows][kPlTile]
     __shared__ float kcen[kMaxLevels], vcen[kMaxLevels];
     __shared__ float red[kPlRows][kPlThreads / 32], rowN[kPlRows], rowA[kPlRows];
@@ -352,7 +362,7 @@ __global__ void __launch_bounds__(kPlThreads) ragged_plain_kernel(RaggedArgs a) 
 
 constexpr int kFinThreads = 512;
 constexpr int kMgRows = 8;       // query rows of a merging CTA, two warps each
-constexpr int kMgParts = 8;      // partials of a row on their way at once
+constexpr int kMgParts = 4;      // partials of a row on their way at once
 constexpr int kWtTokens = 1024;  // tokens of a weighing CTA
 constexpr int kWtRows = 64;      // rows whose normalisers it holds at a time
 
@@ -369,6 +379,8 @@ struct FinishArgs {
     const float *zbuf;
     float *weights;
     int chunks;  // weighing CTAs of a slice
+    float *lse;  // log2 of the rows' normalisers, for weighing CTAs behind the merge (null: they take their own)
+    int csplit;  // merging CTAs of a block of rows, a part of the columns each
 };
 
 // Partials of one row and cache: (N, l, -, -, o[d]) at base + i * step.
@@ -405,7 +417,7 @@ __device__ __forceinline__ float log_sum(const Parts &g, int lane) {
 
 // weights[slice][t] += sum over the slice's rows, in ascending order, of 2^(z - log2 of the row's
 // normaliser), kWtTokens tokens a CTA; bound by the 4 rows + 8 bytes a token that it moves.
-template <int THREADS>
+template <int THREADS, bool LSE>
 __device__ __forceinline__ void weigh_tokens(const FinishArgs &a, unsigned id, float *lse) {
     constexpr int PT = kWtTokens / THREADS;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, ps = partial_stride(a.P.d);
@@ -418,7 +430,8 @@ __device__ __forceinline__ void weigh_tokens(const FinishArgs &a, unsigned id, f
         const int nr = min(kWtRows, R - r0);
         __syncthreads();
         for (int r = warp; r < nr; r += THREADS / 32) {
-            const float x = log_sum(parts_of(a.own, a.own_part, slice, r0 + r, ps), lane);
+            const float x = LSE ? a.lse[(int64_t)slice * R + r0 + r]
+                                : log_sum(parts_of(a.own, a.own_part, slice, r0 + r, ps), lane);
             if (lane == 0) lse[r] = x;
         }
         __syncthreads();
@@ -438,30 +451,36 @@ constexpr int kWtThreads = 256;
 
 __global__ void __launch_bounds__(kWtThreads) serve_weigh_kernel(FinishArgs a) {
     __shared__ float lse[kWtRows];
-    weigh_tokens<kWtThreads>(a, blockIdx.x, lse);
+    grid_wait();
+    weigh_tokens<kWtThreads, true>(a, blockIdx.x, lse);
 }
 
 // Merging CTAs: out = R^T o / l for kMgRows rows.  Two warps a row add its partials, each half of
 // them in the order of the context, rescaled to their largest reference as they come; the rows are
 // then rotated back together, several threads an output.  A row without a token is zero.
 // Latency bound at a few rows: the partials' and R's loads are issued before anything waits.
-__global__ void __launch_bounds__(kFinThreads) serve_finish_kernel(FinishArgs a) {
+__global__ void __launch_bounds__(kFinThreads, 2) serve_finish_kernel(FinishArgs a) {
+    grid_go();
     extern __shared__ __align__(16) float osm[];  // [2][d][kMgRows]
     __shared__ float red[kFinThreads * kMgRows];
     __shared__ float2 head[2][kMgRows];
     if (blockIdx.x >= a.merge_ctas) {
-        weigh_tokens<kFinThreads>(a, blockIdx.x - a.merge_ctas, red);
+        grid_wait();
+        weigh_tokens<kFinThreads, false>(a, blockIdx.x - a.merge_ctas, red);
         return;
     }
     const int d = a.P.d, ps = partial_stride(d), tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int64_t row0 = (int64_t)blockIdx.x * kMgRows;
+    const int64_t row0 = (int64_t)(blockIdx.x / a.csplit) * kMgRows;
     // this thread's column(s) of R^T o and its share of the sum
-    const int ncol = min(d, kFinThreads), ks = kFinThreads / ncol, part = d / ks;
-    const int col = tid % ncol, i0 = tid / ncol * part;
+    const int cw = d / a.csplit, c0 = (int)(blockIdx.x % a.csplit) * cw;
+    const int ncol = min(cw, kFinThreads), ks = min(kFinThreads / ncol, d / 4), part = d / ks;
+    const int col = c0 + tid % ncol, i0 = tid / ncol * part;
+    const bool works = tid / ncol < ks;
     const float *w = a.P.R + (int64_t)i0 * d + col;
     float first[32];
 #pragma unroll
-    for (int k = 0; k < 32; ++k) first[k] = k < part ? w[(int64_t)k * d] : 0.f;
+    for (int k = 0; k < 32; ++k) first[k] = works && k < part ? w[(int64_t)k * d] : 0.f;
+    grid_wait();
     {
         const int r8 = warp >> 1, half = warp & 1;
         const int64_t row = row0 + r8;
@@ -537,9 +556,10 @@ __global__ void __launch_bounds__(kFinThreads) serve_finish_kernel(FinishArgs a)
         const float fx = x.x == -INFINITY ? 0.f : exp2f(x.x - N), fy = y.x == -INFINITY ? 0.f : exp2f(y.x - N);
         const float L = fx * x.y + fy * y.y, inv = L != 0.f ? 1.f / L : 0.f;
         osm[e] = (fx * osm[e] + fy * osm[d * kMgRows + e]) * inv;
+        if (a.lse && e < kMgRows && c0 == 0 && row0 + r < a.rows) a.lse[row0 + r] = L == 0.f ? INFINITY : N + log2f(L);
     }
     __syncthreads();
-    for (int c = col; c < d; c += ncol) {  // one column a thread up to d = 512
+    for (int c = col; c - col < cw; c += ncol) {  // one column a thread up to 512 of them
         float acc[kMgRows] = {};
         const float4 *o4 = (const float4 *)(osm + i0 * kMgRows);
         auto add = [&](float v, int k) {
@@ -553,22 +573,23 @@ __global__ void __launch_bounds__(kFinThreads) serve_finish_kernel(FinishArgs a)
             acc[6] = fmaf(v, y.z, acc[6]);
             acc[7] = fmaf(v, y.w, acc[7]);
         };
-        if (c == col) {
+        if (works && c == col) {
 #pragma unroll
             for (int k = 0; k < 32; ++k)
                 if (k < part) add(first[k], k);
         }
 #pragma unroll 16
-        for (int k = c == col ? 32 : 0; k < part; ++k) add(a.P.R[(int64_t)(i0 + k) * d + c], k);
+        for (int k = c == col ? 32 : 0; works && k < part; ++k) add(a.P.R[(int64_t)(i0 + k) * d + c], k);
 #pragma unroll
-        for (int r = 0; r < kMgRows; ++r) red[(tid / ncol * kMgRows + r) * ncol + col] = acc[r];
+        for (int r = 0; r < kMgRows; ++r)
+            if (works) red[(tid / ncol * kMgRows + r) * ncol + tid % ncol] = acc[r];
         __syncthreads();
         for (int e = tid; e < kMgRows * ncol; e += kFinThreads) {
             const int r = e / ncol, cc = e - r * ncol;
             float v = 0.f;
             for (int k = 0; k < ks; ++k) v += red[(k * kMgRows + r) * ncol + cc];
             if (row0 + r < a.rows) {
-                const int64_t at = (row0 + r) * d + (c - col) + cc;
+                const int64_t at = (row0 + r) * d + c0 + (c - col) + cc;
                 if (a.dtype == TQ_F16) ((__half *)a.out)[at] = __float2half_rn(v);
                 else if (a.dtype == TQ_BF16) ((__nv_bfloat16 *)a.out)[at] = __float2bfloat16_rn(v);
                 else ((float *)a.out)[at] = v;
@@ -636,6 +657,7 @@ cudaError_t launch_ragged_mma(const RaggedArgs &own, const RaggedArgs &prefix, c
     RaggedPair p;
     p.a[0] = own;
     p.a[1] = prefix;
+    p.late_wait = plan.tc.splits > 0;
     auto blocks = [&](const RaggedCache &c) { return (c.rows + plan.row_block - 1) / plan.row_block; };
     p.first = plan.own_ctas ? plan.own_ctas * blocks(own.c) : 0;
     p.total = p.first + (plan.prefix_ctas ? plan.prefix_ctas * blocks(prefix.c) : 0);
@@ -693,6 +715,7 @@ ServePlan plan_serve(const Prepared &P, tq_dtype dtype, int B, int Hq, int Hkv, 
     p.pre_frag = take(p.fast && p.prefix_ctas ? frag_bytes(Hkv, (int64_t)B * R, p.row_block) : 0);
     p.qrows = take(tc ? sizeof(uint16_t) * (size_t)(rows * n) : 0);
     p.fscale = take(sizeof(float) * (size_t)rows);
+    p.lse = take(weigh ? sizeof(float) * (size_t)rows : 0);
     p.zbuf = take(weigh ? sizeof(float) * (size_t)rows * (size_t)t_cap : 0);
     const size_t ps = sizeof(float) * partial_stride(P.d);
     p.own_part = take(p.own_ctas ? ps * ((size_t)p.own_ctas + (size_t)B * Hkv) * R : 0);
@@ -788,7 +811,11 @@ cudaError_t launch_serve(const ServeCall &call, const ServePlan &plan, void *scr
     fa.Hkv = call.Hkv;
     fa.dtype = call.dtype;
     fa.out = call.out;
-    const int64_t merge = (call.rows + kMgRows - 1) / kMgRows;
+    // few rows: the columns of a block of rows go to several CTAs, which merge the same partials each
+    const int64_t blocks = (call.rows + kMgRows - 1) / kMgRows;
+    fa.csplit = 1;
+    while (fa.csplit < P.d / 64 && blocks * fa.csplit * 2 <= kSms) fa.csplit *= 2;
+    const int64_t merge = blocks * fa.csplit;
     int64_t weigh = 0;
     if (call.weights) {
         fa.zbuf = own.zbuf;
@@ -805,11 +832,10 @@ cudaError_t launch_serve(const ServeCall &call, const ServePlan &plan, void *scr
     // Few weighing CTAs ride along with the merging ones; many get a launch of their own, where more of
     // them fit an SM (8 against 1: 11 against 50 us for 2048 of them).
     const bool along = weigh <= kSms;
-    serve_finish_kernel<<<(unsigned)(merge + (along ? weigh : 0)), kFinThreads, fin_smem, s>>>(fa);
-    e = cudaGetLastError();
+    if (!along) fa.lse = (float *)(base + plan.lse);
+    e = launch_after(serve_finish_kernel, (unsigned)(merge + (along ? weigh : 0)), kFinThreads, fin_smem, s, fa);
     if (e != cudaSuccess || along) return e;
-    serve_weigh_kernel<<<(unsigned)weigh, kWtThreads, 0, s>>>(fa);
-    return cudaGetLastError();
+    return launch_after(serve_weigh_kernel, (unsigned)weigh, kWtThreads, 0, s, fa);
 }
 
 }  // namespace tq

@@ -183,7 +183,7 @@ struct ServePlan {
     int prefix_ctas;   // division of the prefix by the ragged kernel (0: not by it)
     PrefixSplit tc;    // splits of the prefix by the many-row kernel (0: not by it)
     // byte offsets in the scratch
-    size_t lens, cum, qprep, own_frag, pre_frag, qrows, fscale, zbuf, own_part, pre_part, total;
+    size_t lens, cum, qprep, own_frag, pre_frag, qrows, fscale, lse, zbuf, own_part, pre_part, total;
 };
 
 ServePlan plan_serve(const Prepared &P, tq_dtype dtype, int B, int Hq, int Hkv, int Nq, int64_t t_prefix,
@@ -207,6 +207,7 @@ int ragged_mma_ctas_per_sm(const Prepared &P);
 // One launch for the own caches and the prefix (those that the plan gives CTAs).
 struct RaggedPair {
     RaggedArgs a[2];
+    int late_wait;     // behind the many-row prefix kernel, which it needs nothing of
     int first, total;  // CTAs of a[0], and of both; CTA i of a cache: division i % ctas, row block i / ctas
 };
 cudaError_t launch_ragged_mma(const RaggedArgs &own, const RaggedArgs &prefix, const ServePlan &plan, bool f32,
