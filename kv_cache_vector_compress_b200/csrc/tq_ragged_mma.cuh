@@ -96,14 +96,21 @@ __global__ void __launch_bounds__(NW * 32, D >= 256 ? 3 : F32 || NT > 1 ? 3 : 4)
     constexpr int VB = C::VB, VN = VB < 3 ? VB : 3;
     extern __shared__ __align__(16) uint8_t smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gid = lane >> 2, t4 = lane & 3;
-    // Behind the many-row prefix kernel this one runs beside it: that kernel lets it start when its own
-    // wait for the preparation is over, and the wait at the end makes the merge wait for both.
-    grid_go();
-    if (!pair.late_wait) grid_wait();
     const bool second = (int)blockIdx.x >= pair.first;
     const RaggedArgs &a = pair.a[second];
     const int id = (int)blockIdx.x - (second ? pair.first : 0), cta = id % a.c.ctas, rblk = id / a.c.ctas;
     const int rblks = (a.c.rows + C::ROWS - 1) / C::ROWS;
+    const ServeTables *T = a.P.serve;
+    const Lut kh = load_lut<(1 << KB)>(T->kh);
+    const Lut kl = load_lut<KB == 3 ? 8 : 1>(T->kl);
+    // 4-bit values: the upper half of the table, magnitudes in ascending order
+    const Lut vh = load_lut<(1 << VN)>(T->vh + (VB == 4 ? 8 : 0));
+    const Lut vl = load_lut<F32 ? (1 << VN) : 1>(T->vl + (VB == 4 ? 8 : 0));
+    const float tau = T->tau;
+    // Behind the many-row prefix kernel this one runs beside it: that kernel lets it start when its own
+    // wait for the preparation is over, and the wait at the end makes the merge wait for both.
+    if (!pair.late_wait) grid_wait();
+    grid_go();
     const int64_t total = ragged_total(a.c);
     const int64_t w1 = cta_first(total, a.c.ctas, cta + 1);
     int64_t w = cta_first(total, a.c.ctas, cta);
@@ -112,13 +119,6 @@ __global__ void __launch_bounds__(NW * 32, D >= 256 ? 3 : F32 || NT > 1 ? 3 : 4)
         return;
     }
     const int r0 = rblk * C::ROWS, nr = min(C::ROWS, a.c.rows - r0);
-    const ServeTables *T = a.P.serve;
-    const Lut kh = load_lut<(1 << KB)>(T->kh);
-    const Lut kl = load_lut<KB == 3 ? 8 : 1>(T->kl);
-    // 4-bit values: the upper half of the table, magnitudes in ascending order
-    const Lut vh = load_lut<(1 << VN)>(T->vh + (VB == 4 ? 8 : 0));
-    const Lut vl = load_lut<F32 ? (1 << VN) : 1>(T->vl + (VB == 4 ? 8 : 0));
-    const float tau = T->tau;
     uint8_t *ring = smem + (size_t)warp * C::NST * C::STAGE;
     float4 *meta = (float4 *)(smem + C::OMETA) + warp * 32;
     uint2 *bfrag = (uint2 *)(smem + C::OB);

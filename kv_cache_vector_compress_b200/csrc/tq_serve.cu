@@ -74,16 +74,17 @@ __device__ __forceinline__ void quarter_dot(float (&v)[kPrepFirst], const float 
     }
 }
 
-// Element c of a row's operands, split hi + lo, into the fragments of row r of a slice.
-__device__ __forceinline__ void put_frag(uint16_t *frag, int64_t slice, int blocks, int block, int d, int kb, int r,
-                                         int c, float v) {
-    const int ks_all = d / 16 + d / 32, nt_all = block / 4;
-    const int blk = r / block, nt = (r % block) / 4, place = frag_place(d, kb, c);
-    const int e = place & 3, t4 = (place >> 2) & 3, ks = place >> 4, gid = 2 * (r & 3);
-    uint16_t *at = frag + ((((slice * blocks + blk) * nt_all + nt) * ks_all + ks) * 32 + 4 * gid + t4) * 4 + e;
+// An operand split hi + lo into the fragments of its row: lo goes to the next column's lane, 4 lanes on.
+__device__ __forceinline__ void put_split(uint16_t *at, float v) {
     const __half hi = __float2half_rn(v);
     at[0] = __half_as_ushort(hi);
-    at[16] = __half_as_ushort(__float2half_rn(v - __half2float(hi)));  // the next gid's lane, 4 lanes on
+    at[16] = __half_as_ushort(__float2half_rn(v - __half2float(hi)));
+}
+
+// Where the fragments of row r of a slice (of `blocks` blocks of `block` rows) begin.
+__device__ __forceinline__ int64_t frag_row(int64_t slice, int blocks, int block, int d, int r) {
+    const int ks_all = d / 16 + d / 32, blk = r / block, nt = (r - blk * block) >> 2;
+    return (((slice * blocks + blk) * (block >> 2) + nt) * ks_all * 32 + 8 * (r & 3)) * 4;
 }
 
 // q_rot = R q and sq = S q in fp32, scaled (see the header), as the attention kernels take them.
@@ -149,6 +150,26 @@ __global__ void __launch_bounds__(kPrepThreads, 3) serve_prep_kernel(PrepArgs a)
     float v[kPrepFirst];
 #pragma unroll
     for (int k = 0; k < kPrepFirst; ++k) v[k] = c < n && k < part ? w[k * ld] : 0.f;
+    // ... and all that does not depend on the sums: the scales, and the places of this warp's results
+    const float qbound = P.serve->qbound, sigma = P.serve->sigma, gamma = sqrtf(1.5707963267948966f) / (float)m;
+    const int64_t row = r0 + warp, slice = row / a.rows_in;
+    const int rr = (int)(row - slice * a.rows_in), b = (int)(slice / a.Hkv), kv = (int)(slice - (int64_t)b * a.Hkv);
+    const int pr = b * a.rows_in + rr;
+    int64_t own_row = 0, pre_row = 0;
+    if (a.own_frag) own_row = frag_row(slice, (a.rows_in + a.row_block - 1) / a.row_block, a.row_block, d, rr);
+    if (a.pre_frag) pre_row = frag_row(kv, a.prefix_blocks, a.row_block, d, pr);
+    const int64_t qrow = ((int64_t)kv * a.B * a.rows_in + pr) * n;
+    int place[2] = {0, 0};  // in 16-bit numbers from the row's beginning
+    if (a.own_frag || a.pre_frag) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int oc = cb + lane + 32 * k;
+            const int at = d == 64    ? frag_place(64, P.kbeta, oc)
+                           : d == 128 ? frag_place(128, P.kbeta, oc)
+                                      : frag_place(256, P.kbeta, oc);
+            place[k] = ((at >> 4) * 32 + ((at >> 2) & 3)) * 4 + (at & 3);
+        }
+    }
     {  // a warp a row
         float mx = 0.f;
         for (int j = lane; j < d; j += 32) {
@@ -171,28 +192,22 @@ __global__ void __launch_bounds__(kPrepThreads, 3) serve_prep_kernel(PrepArgs a)
         for (int r = 0; r < kPrepRows; ++r) red[q4][r][tid & 63] = acc[r];
     }
     __syncthreads();
+    if (warp >= nr) return;
     const int r = warp;
-    if (r >= nr) return;
-    const float bound = rmax[r] * P.serve->qbound * sqrtf((float)d);
+    const float bound = rmax[r] * qbound * sqrtf((float)d);
     const int e = (bound > 0.f && bound < INFINITY) ? min(max(ilogbf(bound) - 14, -126), 126) : 0;
-    const float down = exp2f((float)-e), gamma = sqrtf(1.5707963267948966f) / (float)m, sigma = P.serve->sigma;
-    const int64_t row = r0 + r, slice = row / a.rows_in;
-    const int rr = (int)(row - slice * a.rows_in), b = (int)(slice / a.Hkv), kv = (int)(slice - (int64_t)b * a.Hkv);
+    const float down = exp2f((float)-e);
     if (lane == 0 && cb == 0) a.fscale[row] = a.scale * kLog2eF * exp2f((float)e);
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-        const int cc = lane + 32 * k, c = cb + cc;
-        if (c >= n) break;
+        const int cc = lane + 32 * k, oc = cb + cc;
+        if (oc >= n) break;
         const float x = ((red[0][r][cc] + red[1][r][cc]) + (red[2][r][cc] + red[3][r][cc])) *
-                        ((c < d ? sigma : gamma) * down);
-        if (a.qprep) a.qprep[row * n + c] = x;
-        if (a.own_frag)
-            put_frag(a.own_frag, slice, (a.rows_in + a.row_block - 1) / a.row_block, a.row_block, d, P.kbeta, rr, c, x);
-        if (a.qrows)
-            a.qrows[((int64_t)kv * a.B * a.rows_in + (int64_t)b * a.rows_in + rr) * n + prefix_column(d, c)] =
-                __half_as_ushort(__float2half_rn(x));
-        if (a.pre_frag)
-            put_frag(a.pre_frag, kv, a.prefix_blocks, a.row_block, d, P.kbeta, b * a.rows_in + rr, c, x);
+                        ((oc < d ? sigma : gamma) * down);
+        if (a.qprep) a.qprep[row * n + oc] = x;
+        if (a.own_frag) put_split(a.own_frag + own_row + place[k], x);
+        if (a.pre_frag) put_split(a.pre_frag + pre_row + place[k], x);
+        if (a.qrows) a.qrows[qrow + prefix_column(d, oc)] = __half_as_ushort(__float2half_rn(x));
     }
 }
 
@@ -206,8 +221,7 @@ constexpr int kPlCoord = kMaxDim / kPlThreads;
 // One CTA: its pieces of the slices, for kPlRows query rows (blockIdx.y).  Scores with a thread a
 // token, online softmax, then the weighted value sum with a thread a coordinate; fp32 throughout.
 __global__ void __launch_bounds__(kPlThreads) ragged_plain_kernel(RaggedArgs a) {
-    grid_go();
-    grid_wait();
+    grid_go();  // (launched behind a complete preparation)
     extern __shared__ __align__(16) float sm[];  // qs[(d + m)][kPlRows], ps[kPlRows][kPlTile]
     __shared__ float kcen[kMaxLevels], vcen[kMaxLevels];
     __shared__ float red[kPlRows][kPlThreads / 32], rowN[kPlRows], rowA[kPlRows];
@@ -362,7 +376,7 @@ __global__ void __launch_bounds__(kPlThreads) ragged_plain_kernel(RaggedArgs a) 
 
 constexpr int kFinThreads = 512;
 constexpr int kMgRows = 8;       // query rows of a merging CTA, two warps each
-constexpr int kMgParts = 4;      // partials of a row on their way at once
+constexpr int kMgParts = 8;      // partials of a row on their way at once
 constexpr int kWtTokens = 1024;  // tokens of a weighing CTA
 constexpr int kWtRows = 64;      // rows whose normalisers it holds at a time
 
@@ -424,7 +438,11 @@ __device__ __forceinline__ void weigh_tokens(const FinishArgs &a, unsigned id, f
     const int slice = (int)(id / a.chunks), R = a.own.rows;
     const int len = a.own.len[slice / a.own.per_seq];
     const int t0 = (int)(id - (unsigned)slice * a.chunks) * kWtTokens + tid;
-    if (t0 - tid >= len) return;
+    if (t0 - tid >= len) {
+        grid_wait();
+        return;
+    }
+    grid_wait();
     float s[PT] = {};
     for (int r0 = 0; r0 < R; r0 += kWtRows) {
         const int nr = min(kWtRows, R - r0);
@@ -451,7 +469,6 @@ constexpr int kWtThreads = 256;
 
 __global__ void __launch_bounds__(kWtThreads) serve_weigh_kernel(FinishArgs a) {
     __shared__ float lse[kWtRows];
-    grid_wait();
     weigh_tokens<kWtThreads, true>(a, blockIdx.x, lse);
 }
 
@@ -459,13 +476,12 @@ __global__ void __launch_bounds__(kWtThreads) serve_weigh_kernel(FinishArgs a) {
 // them in the order of the context, rescaled to their largest reference as they come; the rows are
 // then rotated back together, several threads an output.  A row without a token is zero.
 // Latency bound at a few rows: the partials' and R's loads are issued before anything waits.
-__global__ void __launch_bounds__(kFinThreads, 2) serve_finish_kernel(FinishArgs a) {
+__global__ void __launch_bounds__(kFinThreads) serve_finish_kernel(FinishArgs a) {
     grid_go();
     extern __shared__ __align__(16) float osm[];  // [2][d][kMgRows]
     __shared__ float red[kFinThreads * kMgRows];
     __shared__ float2 head[2][kMgRows];
     if (blockIdx.x >= a.merge_ctas) {
-        grid_wait();
         weigh_tokens<kFinThreads, false>(a, blockIdx.x - a.merge_ctas, red);
         return;
     }
@@ -480,8 +496,9 @@ __global__ void __launch_bounds__(kFinThreads, 2) serve_finish_kernel(FinishArgs
     float first[32];
 #pragma unroll
     for (int k = 0; k < 32; ++k) first[k] = works && k < part ? w[(int64_t)k * d] : 0.f;
-    grid_wait();
     {
+        // where the row's partials are: the preparation, whose lengths this takes, is over (the kernel
+        // before lets this one start behind its own wait for it)
         const int r8 = warp >> 1, half = warp & 1;
         const int64_t row = row0 + r8;
         Parts g[2] = {{nullptr, 0, 0}, {nullptr, 0, 0}};
@@ -497,6 +514,7 @@ __global__ void __launch_bounds__(kFinThreads, 2) serve_finish_kernel(FinishArgs
             }
             g[1] = parts_of(a.own, a.own_part, slice, r, ps);
         }
+        grid_wait();
         // the prefix's partials, then the own ones, as one list; this warp's half of it
         const int all = g[0].n + g[1].n, mid = (all + 1) / 2, p0 = half ? mid : 0, p1 = half ? all : mid;
         for (int j0 = 0; j0 < d; j0 += 128) {

@@ -417,21 +417,19 @@ def _row_dtype(dtype: torch.dtype) -> int:
 
 def _arg(t, name: str, dtype: torch.dtype, n: int, dev: int) -> int:
     """The address of t, a contiguous tensor of n values of dtype on CUDA device dev."""
+    if t.dtype is dtype and t.numel() == n and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}")
     if t.numel() != n:
         raise ValueError(f"{name} must hold {n} values, not {t.numel()}")
-    if not t.is_cuda or t.get_device() != dev:
-        raise ValueError(f"{name} must be on CUDA device {dev}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous and on CUDA device {dev}")
 
 
 def _device(p: Params, t: torch.Tensor) -> int:
     """The current device, which must be that of t and of the parameter set."""
     dev = torch.cuda.current_device()
-    if not t.is_cuda or t.get_device() != dev or p.workspace.get_device() != dev:
+    if t.get_device() != dev or p.workspace.get_device() != dev:
         raise ValueError("the tensors and the parameter set must be on the current CUDA device")
     return dev
 
@@ -452,7 +450,7 @@ def _scratch_arg(scratch, need, dev: int):
     """(address, bytes) of the caller's scratch, or of a new one of need() bytes kept in the last place."""
     if scratch is None:
         scratch = torch.empty(max(need(), 16), dtype=torch.uint8, device=dev)
-    elif not scratch.is_cuda or scratch.get_device() != dev:
+    elif scratch.get_device() != dev:
         raise ValueError(f"scratch must be on CUDA device {dev}")
     elif not scratch.is_contiguous():
         raise ValueError("scratch must be contiguous")
@@ -464,7 +462,7 @@ def _status_arg(dev_status, dev: int):
 
 
 def _raw_stream(dev: int) -> int:
-    return torch.cuda.current_stream(dev).cuda_stream
+    return torch._C._cuda_getCurrentRawStream(dev)  # torch.cuda.current_stream(dev).cuda_stream, without its object
 
 
 def tq_attend_shared_scratch_bytes(p: Params, dtype: torch.dtype, B, Hq, Hkv, Nq, t_prefix, t_cap) -> int:
@@ -481,7 +479,7 @@ def tq_attend_shared(p: Params, q: torch.Tensor, prefix_keys, prefix_values, key
     dt, dev = _row_dtype(q.dtype), _device(p, q)
     n = B * Hq * Nq * p.dim
     if out is None:
-        out = torch.empty((B, Hq, Nq, d), dtype=q.dtype, device=q.device)
+        out = torch.empty_like(q)
     pre = _cache_args(p, prefix_keys, prefix_values, Hkv * t_prefix, "prefix", dev) if t_prefix > 0 else (None,) * 6
     own, ln = (None,) * 6, None
     if t_cap > 0:
@@ -509,7 +507,7 @@ def tq_attend_weigh(p: Params, q: torch.Tensor, keys, values, lens: torch.Tensor
     dt, dev = _row_dtype(q.dtype), _device(p, q)
     n = B * Hq * Nq * p.dim
     if out is None:
-        out = torch.empty((B, Hq, Nq, d), dtype=q.dtype, device=q.device)
+        out = torch.empty_like(q)
     own = _cache_args(p, keys, values, B * Hkv * t_cap, "own", dev)
     sc, nb, _keep = _scratch_arg(
         scratch, lambda: tq_attend_weigh_scratch_bytes(p, q.dtype, B, Hq, Hkv, Nq, t_cap), dev)
