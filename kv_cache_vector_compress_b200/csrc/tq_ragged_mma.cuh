@@ -11,8 +11,9 @@
 // codes are interleaved nibble by nibble.
 //
 // Precision.  A query row is split in two fp16 numbers, hi + lo, in two columns of B, whose sums are
-// added: the scores keep 22 bits of Q, and the key operands are exact to 2^-21 (ServeTables: a
-// well chosen scale for 2 bits, a second table for 3 bits).  Value sums: fp16 weights and
+// added: the scores keep 22 bits of Q, and the key operands are exact to 2^-21 for 1 and 2
+// bits (ServeTables: a well chosen scale).  For 3 bits they are off by 3e-5 at most, 8e-6 on average,
+// with that scale; F32 adds a second table, which costs as much again as the first.  Value sums: fp16 weights and
 // centroids for 16-bit outputs; F32 splits both.
 #pragma once
 
@@ -75,13 +76,40 @@ __device__ __forceinline__ void cp_async(void *dst, const void *src) {
                  : "memory");
 }
 
-// `words` words that start at a record, in the widest pieces that every record of W words allows.
+// A warp's copies of an array of W words a record: stage after stage, in the widest pieces that every
+// record is aligned to.
 template <int W>
-__device__ __forceinline__ void copy_words(void *dst, const uint32_t *src, int words, int lane) {
-    constexpr int G = W % 4 == 0 ? 4 : W % 2 == 0 ? 2 : 1;
+struct Copier {
+    static constexpr int G = W % 4 == 0 ? 4 : W % 2 == 0 ? 2 : 1;
+    static constexpr int PIECES = kStage * W / G, N = (PIECES + 31) / 32;
+    const uint32_t *src;  // this lane's first piece of the next stage
+    __device__ __forceinline__ void start(const uint32_t *array, int64_t rec, int lane) { src = array + rec * W + lane * G; }
+    // the next stage, `cnt` records of it; the one after is `step` stages on
+    __device__ __forceinline__ void copy(uint8_t *dst, int cnt, int step, int lane) {
+        uint32_t *d = (uint32_t *)dst + lane * G;
+        if (cnt == kStage) {
 #pragma unroll
-    for (int c = lane; c < kStage * W / G; c += 32)
-        if (c * G < words) cp_async<4 * G>((uint32_t *)dst + c * G, src + c * G);
+            for (int i = 0; i < N; ++i)
+                if (PIECES % 32 == 0 || lane + 32 * i < PIECES) cp_async<4 * G>(d + 32 * i * G, src + 32 * i * G);
+        } else {
+            const int have = cnt * W / G;
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                if (lane + 32 * i < have) cp_async<4 * G>(d + 32 * i * G, src + 32 * i * G);
+        }
+        src += (int64_t)step * kStage * W;
+    }
+};
+
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float lg2(float x) {
+    float r;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
 }
 
 // One CTA: its pieces of the slices (tq_serve.cuh) for one block of ROWS query rows.  Each warp
@@ -102,7 +130,7 @@ __global__ void __launch_bounds__(NW * 32, D >= 256 ? 3 : F32 || NT > 1 ? 3 : 4)
     const int rblks = (a.c.rows + C::ROWS - 1) / C::ROWS;
     const ServeTables *T = a.P.serve;
     const Lut kh = load_lut<(1 << KB)>(T->kh);
-    const Lut kl = load_lut<KB == 3 ? 8 : 1>(T->kl);
+    const Lut kl = load_lut<KB == 3 && F32 ? 8 : 1>(T->kl);
     // 4-bit values: the upper half of the table, magnitudes in ascending order
     const Lut vh = load_lut<(1 << VN)>(T->vh + (VB == 4 ? 8 : 0));
     const Lut vl = load_lut<F32 ? (1 << VN) : 1>(T->vl + (VB == 4 ? 8 : 0));
@@ -132,30 +160,43 @@ __global__ void __launch_bounds__(NW * 32, D >= 256 ? 3 : F32 || NT > 1 ? 3 : 4)
         __syncthreads();  // the last piece's merge is read
         // ---- the warp's stages: pc.s0 + warp, + NW, ...
         const int64_t rec0 = pc.slice * a.c.stride;
-        auto issue = [&](int64_t s) {
-            if (s < pc.s1) {
-                const int t0 = (int)(s * kStage), nt = min(kStage, pc.len - t0);
-                uint8_t *st = ring + (int)((s - pc.s0) / NW % C::NST) * C::STAGE;
-                const int64_t rec = rec0 + t0;
-                copy_words<C::KWPT>(st, a.c.kcodes + rec * C::KWPT, nt * C::KWPT, lane);
-                copy_words<C::SW>(st + C::OS, a.c.ksigns + rec * C::SW, nt * C::SW, lane);
-                copy_words<C::VWPT>(st + C::OV, a.c.vcodes + rec * C::VWPT, nt * C::VWPT, lane);
+        const int64_t first = pc.s0 + warp;
+        // (32-bit counts: a slice has at most 2^26 stages)
+        const int mine = first < pc.s1 ? (int)((pc.s1 - first + NW - 1) / NW) : 0;
+        Copier<C::KWPT> ck;
+        Copier<C::SW> cs;
+        Copier<C::VWPT> cv;
+        ck.start(a.c.kcodes, rec0 + first * kStage, lane);
+        cs.start(a.c.ksigns, rec0 + first * kStage, lane);
+        cv.start(a.c.vcodes, rec0 + first * kStage, lane);
+        const int t_first = (int)(first * kStage);
+        uint32_t fill = 0;  // byte offset of the slot that is filled next
+        auto issue = [&](int i) {
+            if (i < mine) {
+                const int cnt = min(kStage, pc.len - (t_first + i * (NW * kStage)));
+                ck.copy(ring + fill, cnt, NW, lane);
+                cs.copy(ring + fill + C::OS, cnt, NW, lane);
+                cv.copy(ring + fill + C::OV, cnt, NW, lane);
+                fill = fill == (C::NST - 1) * C::STAGE ? 0 : fill + C::STAGE;
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
         };
         uint16_t nk = 0, nrho = 0, nv = 0;  // the next stage's norms, a token a lane
-        auto norms = [&](int64_t s) {
-            const int64_t t = s * kStage + lane;
-            if (s < pc.s1 && t < pc.len) {
-                nk = a.c.knorm[rec0 + t];
-                nrho = a.c.krnorm[rec0 + t];
-                nv = a.c.vnorm[rec0 + t];
+        const uint16_t *pk = a.c.knorm + rec0 + t_first + lane, *pr = a.c.krnorm + rec0 + t_first + lane;
+        const uint16_t *pv = a.c.vnorm + rec0 + t_first + lane;
+        auto norms = [&](int i) {
+            if (i < mine && t_first + i * (NW * kStage) + lane < pc.len) {
+                nk = *pk;
+                nrho = *pr;
+                nv = *pv;
             }
+            pk += NW * kStage;
+            pr += NW * kStage;
+            pv += NW * kStage;
         };
-        const int64_t first = pc.s0 + warp;
 #pragma unroll
-        for (int k = 0; k < C::NST - 1; ++k) issue(first + k * NW);
-        norms(first);
+        for (int k = 0; k < C::NST - 1; ++k) issue(k);
+        norms(0);
         // ---- query fragments of the slice
         const uint2 *qf = a.frag + ((int64_t)pc.slice * rblks + rblk) * (NT * C::KS * 32);
         uint2 breg[C::BREG ? NT * C::KS : 1];
@@ -181,10 +222,11 @@ __global__ void __launch_bounds__(NW * 32, D >= 256 ? 3 : F32 || NT > 1 ? 3 : 4)
                 for (int k = 0; k < 4; ++k) o[t][i][k] = 0.f;
         if constexpr (!C::BREG) __syncthreads();
 
-        for (int64_t s = first; s < pc.s1; s += NW) {
+        uint32_t slot = 0;
+        for (int i_st = 0; i_st < mine; ++i_st) {
             __syncwarp();  // every lane has read the stage whose slot is filled next, and its norms
-            issue(s + (C::NST - 1) * NW);
-            const int t0 = (int)(s * kStage);
+            issue(i_st + C::NST - 1);
+            const int t0 = t_first + i_st * (NW * kStage);
             {
                 // kn, (-rho, -rho), log2 ||v||, 1 / ||v|| (negative where ||v|| is 0); tokens past the
                 // end get y = -inf
@@ -194,14 +236,15 @@ __global__ void __launch_bounds__(NW * 32, D >= 256 ? 3 : F32 || NT > 1 ? 3 : 4)
                 x.x = there ? f16_bits_to_f32(nk) : 0.f;
                 const uint32_t neg = there ? (uint32_t)(nrho ^ 0x8000u) : 0u;
                 x.y = __uint_as_float(neg | (neg << 16));
-                x.z = !there ? -INFINITY : v != v ? v : log2f(vc);
+                x.z = !there ? -INFINITY : v != v ? v : F32 ? log2f(vc) : lg2(vc);
                 x.w = v == 0.f ? -1.f / vc : 1.f / vc;
                 meta[lane] = x;
             }
-            norms(s + NW);
+            norms(i_st + 1);
             asm volatile("cp.async.wait_group %0;" ::"n"(C::NST - 1) : "memory");
             __syncwarp();
-            const uint8_t *st = ring + (int)((s - pc.s0) / NW % C::NST) * C::STAGE;
+            const uint8_t *st = ring + slot;
+            slot = slot == (C::NST - 1) * C::STAGE ? 0 : slot + C::STAGE;
             const uint32_t *skc = (const uint32_t *)st, *sks = (const uint32_t *)(st + C::OS),
                            *svc = (const uint32_t *)(st + C::OV);
             auto bf = [&](int nt, int ks) -> uint2 {
@@ -262,7 +305,7 @@ __global__ void __launch_bounds__(NW * 32, D >= 256 ? 3 : F32 || NT > 1 ? 3 : 4)
                                 look_up(kh, xB[i] >> (16 * h), 0u, a1, a3);
 #pragma unroll
                                 for (int t = 0; t < NT; ++t) mma(acc[t], a0, a1, a2, a3, bf(t, ks));
-                                if constexpr (KB == 3) {
+                                if constexpr (KB == 3 && F32) {
                                     look_up(kl, xA[i] >> (16 * h), 0u, a0, a2);
                                     look_up(kl, xB[i] >> (16 * h), 0u, a1, a3);
 #pragma unroll
@@ -332,8 +375,8 @@ __global__ void __launch_bounds__(NW * 32, D >= 256 ? 3 : F32 || NT > 1 ? 3 : 4)
                     float pA[NT], pB[NT];
 #pragma unroll
                     for (int t = 0; t < NT; ++t) {
-                        pA[t] = exp2f(yA[t] - N[t]);
-                        pB[t] = exp2f(yB[t] - N[t]);
+                        pA[t] = ex2(yA[t] - N[t]);
+                        pB[t] = ex2(yB[t] - N[t]);
                         l[t] = fmaf(pA[t], fabsf(mA.w), l[t]);
                         l[t] = fmaf(pB[t], fabsf(mB.w), l[t]);
                         pA[t] = mA.w < 0.f ? 0.f : pA[t];

@@ -80,7 +80,9 @@ def run_weigh(tq, **kw):
     import torch
     pr = Problem(tq, **kw)
     want, tol, w, wtol = pr.reference(OPERAND[pr.dtype])
-    _, _, _, wtol = pr.reference(0.0)  # the weights keep 32 bits
+    # the weights' scores keep 32 bits, but for the 3-bit key centroids behind 16-bit rows: the best
+    # fp16 table of the four magnitudes has relative errors of 3.06e-5, 1.1e-5, 7.3e-6 and 0
+    _, _, _, wtol = pr.reference(1.55e-5 if pr.bits == 4 and pr.dtype != "f32" else 0.0)
     weights = torch.from_numpy(pr.w0).cuda()
     out = pr.weigh(tq, weights)
     check(out, want, tol, ref.HALF_STEP[pr.dtype], kw)
