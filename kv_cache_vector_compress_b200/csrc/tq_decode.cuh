@@ -71,5 +71,25 @@ __device__ __forceinline__ void look_up(const Lut &t, uint32_t sel, uint32_t fli
     p1 = prmt(l, h, 0x7362);
 }
 
+// x >> 16 on the multiplier (two16 is 2^16, from where the compiler cannot see it): decoding is bound
+// by the pipe that shifts, masks and permutes.
+__device__ __forceinline__ uint32_t half_up(uint32_t x, uint32_t two16) {
+    uint32_t r;
+    asm("mul.hi.u32 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(two16));
+    return r;
+}
+
+// 2-bit codes straight to pairs of fp16 numbers: with a table of four numbers in two registers, code
+// c is its bytes 2 c and 2 c + 1, so the selector of a code is the byte 0x22 c + 0x10, a product.
+// selector(i) has the codes of bits i, i + 8, i + 16 and i + 24.
+struct Pairs2 {
+    uint32_t a, b;  // even and odd bits: fields of two, (w0, w1) of one bit
+    __device__ __forceinline__ Pairs2(uint32_t w0, uint32_t w1)
+        : a(pick(w0, w1 << 1, 0x55555555u)), b(pick(w0 >> 1, w1, 0x55555555u)) {}
+    __device__ __forceinline__ uint32_t selector(int i) const {
+        return (((i & 1 ? b : a) >> (i & 6)) & 0x03030303u) * 0x22u + 0x10101010u;
+    }
+};
+
 }  // namespace decode
 }  // namespace tq

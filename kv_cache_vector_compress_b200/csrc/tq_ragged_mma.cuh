@@ -135,6 +135,9 @@ __global__ void __launch_bounds__(NW * 32, D >= 256 ? 3 : F32 || NT > 1 ? 3 : 4)
     const Lut vh = load_lut<(1 << VN)>(T->vh + (VB == 4 ? 8 : 0));
     const Lut vl = load_lut<F32 ? (1 << VN) : 1>(T->vl + (VB == 4 ? 8 : 0));
     const float tau = T->tau;
+    // 2-bit keys: the four centroids as pairs of bytes; 2^16 where the compiler does not see it
+    const uint32_t kp0 = T->kh[0] | ((uint32_t)T->kh[1] << 16), kp1 = T->kh[2] | ((uint32_t)T->kh[3] << 16);
+    const uint32_t k16 = pair.two16;
     // Behind the many-row prefix kernel this one runs beside it: that kernel lets it start when its own
     // wait for the preparation is over, and the wait at the end makes the merge wait for both.
     if (!pair.late_wait) grid_wait();
@@ -155,7 +158,7 @@ __global__ void __launch_bounds__(NW * 32, D >= 256 ? 3 : F32 || NT > 1 ? 3 : 4)
     const int vhalf = D >= 256 ? 0 : D == 128 ? gid & 1 : (gid >> 1) & 1;
 
     Piece pc;
-    for (; w < w1; w += pc.s1 - pc.s0) {
+    for (; w < w1; w += pc.counted) {
         pc = piece_at(a.c, w, w1);
         __syncthreads();  // the last piece's merge is read
         // ---- the warp's stages: pc.s0 + warp, + NW, ...
@@ -247,6 +250,7 @@ __global__ void __launch_bounds__(NW * 32, D >= 256 ? 3 : F32 || NT > 1 ? 3 : 4)
             slot = slot == (C::NST - 1) * C::STAGE ? 0 : slot + C::STAGE;
             const uint32_t *skc = (const uint32_t *)st, *sks = (const uint32_t *)(st + C::OS),
                            *svc = (const uint32_t *)(st + C::OV);
+            auto up = [&](uint32_t x, int kk) { return kk ? half_up(x, k16) : x; };
             auto bf = [&](int nt, int ks) -> uint2 {
                 if constexpr (C::BREG) return breg[nt * C::KS + ks];
                 else return bfrag[(nt * C::KS + ks) * 32 + lane];
@@ -283,6 +287,18 @@ __global__ void __launch_bounds__(NW * 32, D >= 256 ? 3 : F32 || NT > 1 ? 3 : 4)
                             const uint32_t a3 = ((wB[0] << (PR - 2 - 2 * k)) & 0x80008000u) ^ one;
 #pragma unroll
                             for (int t = 0; t < NT; ++t) mma(acc[t], a0, a1, a2, a3, bf(t, gg * (PR / 2) + k));
+                        }
+                    } else if constexpr (KB == 2) {
+                        constexpr int NP = D >= 128 ? 8 : 4;
+                        const int sh = D >= 128 ? 0 : 4 * (t4 & 1);
+                        Pairs2 sA(wA[0] >> sh, wA[KB - 1] >> sh), sB(wB[0] >> sh, wB[KB - 1] >> sh);
+#pragma unroll
+                        for (int i = 0; i < NP; ++i) {
+                            const uint32_t uA = sA.selector(i), uB = sB.selector(i);
+                            const uint32_t a0 = prmt(kp0, kp1, uA), a1 = prmt(kp0, kp1, uB);
+                            const uint32_t a2 = prmt(kp0, kp1, half_up(uA, k16)), a3 = prmt(kp0, kp1, half_up(uB, k16));
+#pragma unroll
+                            for (int t = 0; t < NT; ++t) mma(acc[t], a0, a1, a2, a3, bf(t, gg * NP + i));
                         }
                     } else {
                         if (D < 128) {
@@ -439,13 +455,13 @@ __global__ void __launch_bounds__(NW * 32, D >= 256 ? 3 : F32 || NT > 1 ? 3 : 4)
                             const uint32_t f0 = VB == 4 ? prmt(0x80u, 0u, sg[0] >> (16 * kk)) : 0u;
                             const uint32_t f1 = VB == 4 ? prmt(0x80u, 0u, sg[1] >> (16 * kk)) : 0u;
                             uint32_t a0, a1, a2, a3;
-                            look_up(vh, x[0][i] >> (16 * kk), f0, a0, a1);
-                            look_up(vh, x[1][i] >> (16 * kk), f1, a2, a3);
+                            look_up(vh, up(x[0][i], kk), f0, a0, a1);
+                            look_up(vh, up(x[1][i], kk), f1, a2, a3);
 #pragma unroll
                             for (int t = 0; t < C::NO; ++t) mma(o[t][tile], a0, a1, a2, a3, pb[t]);
                             if constexpr (F32) {
-                                look_up(vl, x[0][i] >> (16 * kk), f0, a0, a1);
-                                look_up(vl, x[1][i] >> (16 * kk), f1, a2, a3);
+                                look_up(vl, up(x[0][i], kk), f0, a0, a1);
+                                look_up(vl, up(x[1][i], kk), f1, a2, a3);
 #pragma unroll
                                 for (int t = 0; t < C::NO; ++t) mma(o[t][tile], a0, a1, a2, a3, pb[t]);
                             }

@@ -114,7 +114,7 @@ __global__ void __launch_bounds__(kPrepThreads, 3) serve_prep_kernel(PrepArgs a)
                 }
                 a.len_own[b] = (int32_t)len;
             }
-            const int64_t st = (len + kStage - 1) / kStage;
+            const int64_t st = counted_stages(len);
             int64_t x = st;
             for (int o = 1; o < 32; o <<= 1) {
                 const int64_t y = __shfl_up_sync(kFull, x, o);
@@ -135,7 +135,7 @@ __global__ void __launch_bounds__(kPrepThreads, 3) serve_prep_kernel(PrepArgs a)
             a.cum_own[a.B] = before;
             a.len_own[a.B] = (int32_t)a.t_prefix;
             a.cum_own[a.B + 1] = 0;
-            a.cum_own[a.B + 2] = (a.t_prefix + kStage - 1) / kStage;
+            a.cum_own[a.B + 2] = counted_stages(a.t_prefix);
         }
         return;
     }
@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(kPlThreads) ragged_plain_kernel(RaggedArgs a) 
     const int r0 = blockIdx.y * kPlRows, nr = min(kPlRows, a.c.rows - r0);
     const int kw = P.kbeta * (d >> 5), sw = m >> 5, vw = P.vbeta * (d >> 5);
     Piece pc;
-    for (int64_t w = cta_first(total, a.c.ctas, blockIdx.x); w < w1; w += pc.s1 - pc.s0) {
+    for (int64_t w = cta_first(total, a.c.ctas, blockIdx.x); w < w1; w += pc.counted) {
         pc = piece_at(a.c, w, w1);
         const int64_t rec0 = pc.slice * a.c.stride;
         const int t_end = (int)min((int64_t)pc.len, pc.s1 * kStage);
@@ -675,6 +675,7 @@ cudaError_t launch_ragged_mma(const RaggedArgs &own, const RaggedArgs &prefix, c
     RaggedPair p;
     p.a[0] = own;
     p.a[1] = prefix;
+    p.two16 = 1u << 16;
     p.late_wait = plan.tc.splits > 0;
     auto blocks = [&](const RaggedCache &c) { return (c.rows + plan.row_block - 1) / plan.row_block; };
     p.first = plan.own_ctas ? plan.own_ctas * blocks(own.c) : 0;

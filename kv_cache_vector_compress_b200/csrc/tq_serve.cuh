@@ -43,7 +43,7 @@ struct RaggedCache {
     int rows, rows_in;
     int64_t rows_outer;
     const int32_t *len;  // device, [nseq], within [0, stride]
-    const int64_t *cum;  // device, [nseq + 1]: stages of the sequences before (of one slice each)
+    const int64_t *cum;  // device, [nseq + 1]: counted stages of the sequences before (of one slice each)
     int ctas;            // CTAs the stages of all slices are divided among
 };
 
@@ -53,11 +53,18 @@ __device__ __forceinline__ int64_t ragged_row(const RaggedCache &c, int slice, i
 
 // The W stages of all slices, in order, are divided evenly among G = min(ctas, W) CTAs, so that none
 // of these is without work; CTA i takes stages [i W / G, (i + 1) W / G) and so a piece of one or
-// more slices.  Slice s's piece in CTA i has the partial number i + s: from one piece to the next
+// more slices.  A slice that is not empty counts kPieceCost stages more than it has, in front, for
+// what a piece costs besides its stages (its first loads, its partial result).  Slice s's piece in CTA i has the partial number i + s: from one piece to the next
 // either i or s grows, so no two pieces share one.
+constexpr int kPieceCost = 3;
+__host__ __device__ constexpr int64_t counted_stages(int64_t tokens) {
+    return tokens > 0 ? (tokens + kStage - 1) / kStage + kPieceCost : 0;
+}
+
 struct Piece {
     int slice;
-    int64_t s0, s1;  // stages of the slice
+    int64_t s0, s1;  // stages of the slice (there may be none)
+    int64_t counted;  // what the piece counts in the division
     int len;         // tokens of the slice
 };
 
@@ -81,9 +88,10 @@ __device__ __forceinline__ Piece piece_at(const RaggedCache &c, int64_t w, int64
     const int64_t h = (w - base) / n;
     Piece p;
     p.slice = (int)(lo * (int64_t)c.per_seq + h);
-    p.s0 = w - base - h * n;
-    const int64_t left = w1 - w;
-    p.s1 = p.s0 + left < n ? p.s0 + left : n;
+    const int64_t v0 = w - base - h * n, v1 = v0 + (w1 - w) < n ? v0 + (w1 - w) : n;
+    p.counted = v1 - v0;
+    p.s0 = v0 > kPieceCost ? v0 - kPieceCost : 0;
+    p.s1 = v1 > kPieceCost ? v1 - kPieceCost : 0;
     p.len = c.len[lo];
     return p;
 }
@@ -105,14 +113,19 @@ __device__ __forceinline__ bool slice_ctas(const RaggedCache &c, int slice, int 
 // laid out the way the kernels decode the packed words.
 
 // Register kernels (tq_ragged_mma.cuh): element e (0..3) of lane t4's operand in product ks of the
-// code part.  A lane takes whole words (half a word at 64 coordinates); nibble 4 h + e of selector i
-// holds bit 4 (4 h + e) + i of a word.  1-bit codes are taken as the signs are.
+// code part.  A lane takes whole words (half a word at 64 coordinates).  3-bit codes: nibble 4 h + e
+// of selector i holds bit 4 (4 h + e) + i of a word.  2-bit codes: byte e of selector i holds bit
+// 8 e + i.  1-bit codes are taken as the signs are.
 __host__ __device__ constexpr int frag_code_coord(int D, int KB, int t4, int ks, int e) {
     const int ng = D >= 128 ? D / 128 : 1;
     if (KB == 1) {
         const int pairs = D >= 128 ? 16 : 8, j = 2 * ks + (e >> 1);
         const int g = D >= 128 ? t4 * ng + j / pairs : t4 >> 1;
         return 32 * g + (D >= 128 ? 0 : 8 * (t4 & 1)) + j % pairs + 16 * (e & 1);
+    }
+    if (KB == 2) {
+        const int ni = D >= 128 ? 8 : 4, g = D >= 128 ? t4 * ng + ks / ni : t4 >> 1;
+        return 32 * g + 8 * e + ks % ni + (D >= 128 ? 0 : 4 * (t4 & 1));
     }
     const int ni = D >= 128 ? 4 : 2, h = ks & 1, i = (ks >> 1) % ni;
     const int g = D >= 128 ? t4 * ng + (ks >> 1) / ni : t4 >> 1;
@@ -136,6 +149,11 @@ __host__ __device__ constexpr int frag_place(int D, int KB, int c) {
         const int t4 = D >= 128 ? g / ng : 2 * g + (l >> 3);
         const int j = (D >= 128 ? (g % ng) * pairs : 0) + l % pairs;
         return 4 * (4 * (j / 2) + t4) + 2 * (j & 1) + up;
+    }
+    if (KB == 2) {
+        const int i8 = bit & 7, t4 = D >= 128 ? g / ng : 2 * g + (i8 >> 2);
+        const int ks = D >= 128 ? (g % ng) * 8 + i8 : i8 & 3;
+        return 4 * (4 * ks + t4) + (bit >> 3);
     }
     const int ni = D >= 128 ? 4 : 2, nib = bit >> 2, i4 = bit & 3;
     const int t4 = D >= 128 ? g / ng : 2 * g + (i4 >> 1), i = D >= 128 ? i4 : i4 & 1;
@@ -207,6 +225,7 @@ int ragged_mma_ctas_per_sm(const Prepared &P);
 // One launch for the own caches and the prefix (those that the plan gives CTAs).
 struct RaggedPair {
     RaggedArgs a[2];
+    uint32_t two16;    // 65536
     int late_wait;     // behind the many-row prefix kernel, which it needs nothing of
     int first, total;  // CTAs of a[0], and of both; CTA i of a cache: division i % ctas, row block i / ctas
 };
