@@ -136,20 +136,36 @@ __device__ __forceinline__ void ld_done(uint32_t (&r)[32]) {
                  : "memory");
 }
 
-// mbar_wait in which a try may sleep for up to 4 us: the waiting warps share their schedulers with
-// the decoders, and with plain tries 3 of 10 issued instructions were theirs.
+// Eight tries at a barrier's phase, two instructions each.
+__device__ __forceinline__ bool try_wait8(uint32_t addr, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t@p bra DONE;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t@p bra DONE;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t@p bra DONE;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t@p bra DONE;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t@p bra DONE;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t@p bra DONE;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t@p bra DONE;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "DONE:\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(addr), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
+// mbar_wait with the flag and the clock looked at after every 64 tries only: waiting warps share
+// their schedulers, and the pipe that decodes, with the decoders.
 __device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity, volatile int *abort) {
     const uint32_t b = smem_u32(bar);
-    if (mbar_try_wait(b, parity)) return true;
+    if (try_wait8(b, parity)) return true;
     const uint64_t t0 = globaltimer();
     while (true) {
-        uint32_t done;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(done)
-            : "r"(b), "r"(parity), "r"(4000u)
-            : "memory");
-        if (done) return true;
+#pragma unroll 1
+        for (int i = 0; i < 8; ++i)
+            if (try_wait8(b, parity)) return true;
         if (*abort) return false;
         if (globaltimer() - t0 > kTimeoutNs) {
             *abort = 1;
@@ -171,6 +187,16 @@ __device__ __forceinline__ void store_pairs(uint32_t at, uint32_t a, uint32_t b,
 }
 
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// mma_ts by the lanes that have `lead` set.
+__device__ __forceinline__ void mma_ts_if(uint32_t lead, uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                          uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(lead)
+        : "memory");
+}
 
 // Byte offset of 16-byte chunk c of token t in a tile of operand columns (128-byte swizzle).
 template <uint32_t BLK>
@@ -263,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(PrefixArgs a) {
     }
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_s;
+    const uint32_t tmem = __shfl_sync(kFull, *tmem_s, 0);
 
     if (warp < kSmWarps) {
         // ------------------------------------------------------------ softmax
@@ -600,21 +626,28 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(PrefixArgs a) {
             if (j + 1 < nT) decode_tile(j + 1, std::integral_constant<int, 1>{});
         }
         asm volatile("cp.async.wait_group 0;" ::: "memory");
-    } else if (lane == 0) {
+    } else {
         // ------------------------------------------------------------ MMAs
+        // The whole warp runs this and its first lane issues: descriptors stay warp-uniform, an add of
+        // a constant each.
         const uint32_t sbase = smem_u32(sm);
         constexpr uint32_t is = idesc_f16_f32(128, TT), iv = idesc_f16_f32(128, D) | (1u << 16);
+        const uint32_t lead = lane == 0 ? 1u : 0u;
+        const uint64_t kd0 = sdesc_sw128(sbase), vd0 = sdesc_mn(sbase + C::OV, C::BLK);
         auto scores = [&](int j) -> bool {
             const int st = j & 1, sb = j % C::SB;
             if (!wait_for(&bars[kKFull + st], (j >> 1) & 1, abort_s)) return false;
             tc_fence_after();
-            const uint32_t kb = sbase + st * C::KST;
+            const uint64_t kd = kd0 + (uint64_t)(st * (C::KST >> 4));
+            const uint32_t acc = tmem + C::CS + sb * TT;
 #pragma unroll
             for (int k = 0; k < C::K / 16; ++k)
-                mma_ts(tmem + C::CS + sb * TT, tmem + C::CQ + 8 * k, sdesc_sw128(kb + (k >> 2) * C::BLK + (k & 3) * 32), is,
-                       k ? 1u : 0u);
-            mma_commit(&bars[kKEmpty + st]);
-            mma_commit(&bars[kSFull + sb]);
+                mma_ts_if(lead, acc, tmem + C::CQ + 8 * k, kd + (((k >> 2) * C::BLK + (k & 3) * 32) >> 4), is, k ? 1u : 0u);
+            if (lead) {
+                mma_commit(&bars[kKEmpty + st]);
+                mma_commit(&bars[kSFull + sb]);
+            }
+            __syncwarp();
             return true;
         };
         // Q arrived as phase 0 of the last score buffer's W barrier
@@ -623,20 +656,19 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(PrefixArgs a) {
             const int st = j & 1, sb = j % C::SB;
             // The next scores go over the weights of tile j - 1, behind their product: one thread's MMAs
             // run in the order in which they are issued.
-            if (C::SB == 2 && j + 1 < nT)
-                ok = scores(j + 1);
+            if (C::SB == 2 && j + 1 < nT) ok = scores(j + 1);
             const uint32_t ph = (uint32_t)(j / C::SB + (sb == C::SB - 1 ? 1 : 0)) & 1;
             ok = ok && wait_for(&bars[kVFull + st], (j >> 1) & 1, abort_s) && wait_for(&bars[kPFull + sb], ph, abort_s);
             if (!ok) break;
             tc_fence_after();
-            const uint32_t vb = sbase + C::OV + st * C::VST;
+            const uint64_t vd = vd0 + (uint64_t)(st * (C::VST >> 4));
 #pragma unroll
             for (int k = 0; k < TT / 16; ++k)
-                mma_ts(tmem + C::CO, tmem + C::CS + sb * TT + 8 * k, sdesc_mn(vb + k * 2048, C::BLK), iv,
-                       (j | k) ? 1u : 0u);
-            mma_commit(&bars[kVEmpty + st]);
-            if (C::SB == 1 && j + 1 < nT)
-                ok = wait_for(&bars[kVEmpty + st], (j >> 1) & 1, abort_s) && scores(j + 1);
+                mma_ts_if(lead, tmem + C::CO, tmem + C::CS + sb * TT + 8 * k, vd + (k * 2048 >> 4), iv,
+                          (j | k) ? 1u : 0u);
+            if (lead) mma_commit(&bars[kVEmpty + st]);
+            __syncwarp();
+            if (C::SB == 1 && j + 1 < nT) ok = scores(j + 1);
         }
     }
     __syncthreads();
