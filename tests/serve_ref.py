@@ -111,11 +111,11 @@ def attend(q, R, S, caches, Hkv, scale, operand=0.0):
             rel = 2 * e.max(1, keepdims=True) + (T + 16) * u
             rel = np.expm1(np.minimum(rel, 50.0)) + 4 * u * np.abs(z).max(1, keepdims=True)  # a logit itself is rounded to fp32
             o = w @ v
-            # 16-bit weights and centroids.  A weight (with its value norm) is held relative to at
-            # least 2^-8 of the largest, and fp16's numbers are 2^-24 apart at the low end.
+            # 16-bit weights and values.  A weight is held relative to at least 2^-8 of the largest, a
+            # value to its tile's largest, and fp16's numbers are 2^-24 apart at the low end.
             eo = (w @ np.abs(v)) * (rel + 2 * operand)
             if operand:
-                eo += T * u * (w * np.abs(v).max(1)).max(1, keepdims=True)
+                eo += T * u * w.max(1, keepdims=True) * np.abs(v).max()
             out[b, h * G:(h + 1) * G] = (o @ R).reshape(G, Nq, d)
             tol[b, h * G:(h + 1) * G] = ((eo + d * u * np.abs(o)) @ np.abs(R)).reshape(G, Nq, d)
             n = z.shape[1] - sum(k.shape[1] for k in K[:-1])

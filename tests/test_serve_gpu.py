@@ -284,6 +284,69 @@ def test_graph_follows_the_lengths(tq):
         assert ev[4].tolist() == [min(n, 120) for n in lens]
 
 
+def test_offsets_past_32_bits(tq):
+    """Caches whose arrays are longer than 2^31 words and 2^32 bytes: the last sequence's records lie
+    behind both (only the tokens in use are ever written)."""
+    import torch
+    B, d, bits, cap, n = 3, 256, 4, 46_000_000, 100
+    pr = Problem(tq, dtype="bf16", d=d, bits=bits, B=B, Hq=2, Hkv=1, t_cap=n, lens=[40, 100, 71], seed=41)
+    assert 2 * cap * pr.p.key_words() > 2 ** 31
+
+    def spread(t):
+        big = torch.empty((B * cap, *t.shape[1:]), dtype=t.dtype, device="cuda")
+        big.view(B, cap, *t.shape[1:])[:, :n] = t.view(B, n, *t.shape[1:])
+        return big
+
+    k, v = tuple(map(spread, pr.k)), tuple(map(spread, pr.v))
+    w = torch.zeros(B, 1, cap, device="cuda")
+    out = tq.tq_attend_weigh(pr.p, pr.q, k, v, pr.dlens, 1, cap, w)
+    want, tol, ws, wtol = pr.reference(OPERAND["bf16"])
+    check(out, want, tol, ref.HALF_STEP["bf16"], "weigh")
+    got = tq.tq_attend_shared(pr.p, pr.q, None, None, k, v, pr.dlens, 1, 0, cap)
+    check(got, want, tol, ref.HALF_STEP["bf16"], "shared")
+    _, _, _, wtol = pr.reference(1.55e-5)  # as in run_weigh
+    check(w[:, :, :n].contiguous(), ws, wtol, 2.0 ** -23, "weights")
+    assert torch.count_nonzero(w[:, :, n:]) == 0
+    ok, ov, ow, kept, lens = tq.tq_evict(pr.p, k, v, w, pr.dlens, 1, cap, 50, 5, 60)
+    keep = ref.evict(w[:, :, :n].cpu().numpy(), pr.lens, 50, 5)
+    for b in range(B):
+        s = keep[b][0]
+        assert kept[b, 0, :len(s)].tolist() == s.tolist() and lens[b].item() == len(s)
+        for dst, src in zip((*ok, *ov), (*pr.k, *pr.v)):
+            assert torch.equal(dst.view(B, 60, -1)[b, :len(s)], src.view(B, n, -1)[b, torch.from_numpy(s).cuda()])
+
+
+@pytest.mark.parametrize("dtype,B", [("bf16", 40), ("f32", 3)])
+def test_law_of_the_codebook(tq, dtype, B):
+    """The codebooks of the exact coordinate law go through the same tables."""
+    import oracle
+    import torch
+    pr = Problem(tq, dtype=dtype, d=64, bits=3, B=B, Hq=4, Hkv=1, t_prefix=150, t_cap=20, seed=43)
+    gaussian = pr.shared(tq)
+    pr.p = tq.Params(64, 3, 32, torch.from_numpy(pr.R).cuda(), torch.from_numpy(pr.S).cuda(), law="beta")
+    out = pr.shared(tq)
+    assert not torch.equal(out, gaussian)
+    plain = oracle.codebook_f32
+    try:
+        oracle.codebook_f32 = lambda dim, bits: plain(dim, bits, law="beta")
+        want, tol, _, _ = pr.reference(OPERAND[dtype])
+    finally:
+        oracle.codebook_f32 = plain
+    check(out, want, tol, ref.HALF_STEP[dtype], (dtype, B))
+
+
+def test_softmax_scale(tq):
+    import torch
+    pr = Problem(tq, dtype="f32", B=12, Hq=4, Hkv=2, t_prefix=90, t_cap=30, seed=44)
+    pr.scale = 0.7
+    for op in ("shared", "weigh"):
+        if op == "weigh":
+            pr.pre = None
+        want, tol, _, _ = pr.reference(0.0)
+        out = pr.shared(tq, scale=0.7) if op == "shared" else pr.weigh(tq, torch.from_numpy(pr.w0).cuda(), scale=0.7)
+        check(out, want, tol, ref.HALF_STEP["f32"], op)
+
+
 # ------------------------------------------------------------------- eviction
 
 def run_evict(tq, weights, lens, budget, recent, out_cap, d=128, bits=3, seed=0):
