@@ -8,6 +8,7 @@
 
 #include <cuda_bf16.h>
 
+#include "tq_f32x2.cuh"
 #include "tq_launch.cuh"
 #include "tq_serve.cuh"
 
@@ -18,7 +19,6 @@ namespace {
 // ------------------------------------------------------------------ preparation
 
 constexpr int kPrepThreads = 256;
-constexpr int kPrepRows = 8;   // query rows of a CTA
 constexpr int kPrepCols = 64;  // operands of a CTA; 4 threads share one, a quarter of the sum each
 
 struct PrepArgs {
@@ -48,12 +48,13 @@ __device__ __forceinline__ float load_elem(const void *p, tq_dtype t, int64_t i)
     return ((const float *)p)[i];
 }
 
-// Sum over this thread's quarter of the coordinates j of w[j ld] x[j][0..7]: the first of w's loads
-// are in v already, the others go CH at a time.
+// Sums over this thread's quarter of the coordinates j of w[j ld] x[j][row], two rows a number: the
+// first of w's loads are in v already, the others go CH at a time.
 constexpr int kPrepFirst = 32;
-template <int CH>
+template <int CH, int ROWS>
 __device__ __forceinline__ void quarter_dot(float (&v)[kPrepFirst], const float *w, int64_t ld, const float *x,
-                                            int count, float (&acc)[kPrepRows]) {
+                                            int count, f2 (&acc)[ROWS / 2]) {
+#pragma unroll 1
     for (int j0 = 0; j0 < count; j0 += CH) {
         if (j0 > 0) {
 #pragma unroll
@@ -61,15 +62,13 @@ __device__ __forceinline__ void quarter_dot(float (&v)[kPrepFirst], const float 
         }
 #pragma unroll
         for (int k = 0; k < CH; ++k) {
-            const float4 a = *(const float4 *)(x + (j0 + k) * kPrepRows), b = *(const float4 *)(x + (j0 + k) * kPrepRows + 4);
-            acc[0] = fmaf(v[k], a.x, acc[0]);
-            acc[1] = fmaf(v[k], a.y, acc[1]);
-            acc[2] = fmaf(v[k], a.z, acc[2]);
-            acc[3] = fmaf(v[k], a.w, acc[3]);
-            acc[4] = fmaf(v[k], b.x, acc[4]);
-            acc[5] = fmaf(v[k], b.y, acc[5]);
-            acc[6] = fmaf(v[k], b.z, acc[6]);
-            acc[7] = fmaf(v[k], b.w, acc[7]);
+            const f2 vv = pack2(v[k], v[k]);
+#pragma unroll
+            for (int r = 0; r < ROWS / 4; ++r) {
+                const float4 y = *(const float4 *)(x + (j0 + k) * ROWS + 4 * r);
+                acc[2 * r] = fma2(vv, pack2(y.x, y.y), acc[2 * r]);
+                acc[2 * r + 1] = fma2(vv, pack2(y.z, y.w), acc[2 * r + 1]);
+            }
         }
     }
 }
@@ -88,9 +87,11 @@ __device__ __forceinline__ int64_t frag_row(int64_t slice, int blocks, int block
 }
 
 // q_rot = R q and sq = S q in fp32, scaled (see the header), as the attention kernels take them.
-// A CTA computes kPrepCols operands of kPrepRows rows: latency bound at a few rows (three dependent
-// steps: the rows, the loads of R^T in flight together, the exchange of the quarters), and at many
-// by its reads of R^T and S^T from L2.  The last CTA lays out the contexts instead.
+// A CTA computes kPrepCols operands of kPrepRows rows (8, or 16 when there are many): latency bound at
+// a few rows (three dependent steps: the rows, the loads of R^T in flight together, the exchange of
+// the quarters; 4.3 us), and at many by its reads of R^T and S^T from L2 (d = 128: 9.4 us for 1024
+// rows, 14 us for 2048 in blocks of 16).  The last CTA lays out the contexts instead.
+template <int kPrepRows>
 __global__ void __launch_bounds__(kPrepThreads, 3) serve_prep_kernel(PrepArgs a) {
     grid_go();
     extern __shared__ __align__(16) float qT[];  // [d][kPrepRows]
@@ -150,16 +151,9 @@ __global__ void __launch_bounds__(kPrepThreads, 3) serve_prep_kernel(PrepArgs a)
     float v[kPrepFirst];
 #pragma unroll
     for (int k = 0; k < kPrepFirst; ++k) v[k] = c < n && k < part ? w[k * ld] : 0.f;
-    // ... and all that does not depend on the sums: the scales, and the places of this warp's results
+    // ... and all that does not depend on the sums: the scales and the places of this warp's results
     const float qbound = P.serve->qbound, sigma = P.serve->sigma, gamma = sqrtf(1.5707963267948966f) / (float)m;
-    const int64_t row = r0 + warp, slice = row / a.rows_in;
-    const int rr = (int)(row - slice * a.rows_in), b = (int)(slice / a.Hkv), kv = (int)(slice - (int64_t)b * a.Hkv);
-    const int pr = b * a.rows_in + rr;
-    int64_t own_row = 0, pre_row = 0;
-    if (a.own_frag) own_row = frag_row(slice, (a.rows_in + a.row_block - 1) / a.row_block, a.row_block, d, rr);
-    if (a.pre_frag) pre_row = frag_row(kv, a.prefix_blocks, a.row_block, d, pr);
-    const int64_t qrow = ((int64_t)kv * a.B * a.rows_in + pr) * n;
-    int place[2] = {0, 0};  // in 16-bit numbers from the row's beginning
+    int place[2] = {0, 0};  // of operands cb + lane and + 32, in 16-bit numbers from the row's beginning
     if (a.own_frag || a.pre_frag) {
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
@@ -170,44 +164,56 @@ __global__ void __launch_bounds__(kPrepThreads, 3) serve_prep_kernel(PrepArgs a)
             place[k] = ((at >> 4) * 32 + ((at >> 2) & 3)) * 4 + (at & 3);
         }
     }
-    {  // a warp a row
+    for (int r = warp; r < kPrepRows; r += kPrepThreads / 32) {  // a warp a row
         float mx = 0.f;
         for (int j = lane; j < d; j += 32) {
-            const float x = warp < nr ? load_elem(a.q, a.dtype, (r0 + warp) * d + j) : 0.f;
-            qT[j * kPrepRows + warp] = x;
+            const float x = r < nr ? load_elem(a.q, a.dtype, (r0 + r) * d + j) : 0.f;
+            qT[j * kPrepRows + r] = x;
             mx = fmaxf(mx, fabsf(x));
         }
         mx = warp_max(mx);
-        if (lane == 0) rmax[warp] = mx;
+        if (lane == 0) rmax[r] = mx;
     }
     __syncthreads();
     {
-        float acc[kPrepRows] = {};
+        f2 acc[kPrepRows / 2];
+#pragma unroll
+        for (int r = 0; r < kPrepRows / 2; ++r) acc[r] = pack2(0.f, 0.f);
         if (c < n) {
             const float *x = qT + q4 * part * kPrepRows;
-            if (part >= 32) quarter_dot<32>(v, w, ld, x, part, acc);
-            else quarter_dot<8>(v, w, ld, x, part, acc);
+            if (part >= 32) quarter_dot<32, kPrepRows>(v, w, ld, x, part, acc);
+            else quarter_dot<8, kPrepRows>(v, w, ld, x, part, acc);
         }
 #pragma unroll
-        for (int r = 0; r < kPrepRows; ++r) red[q4][r][tid & 63] = acc[r];
+        for (int r = 0; r < kPrepRows / 2; ++r) unpack2(acc[r], red[q4][2 * r][tid & 63], red[q4][2 * r + 1][tid & 63]);
     }
     __syncthreads();
-    if (warp >= nr) return;
-    const int r = warp;
-    const float bound = rmax[r] * qbound * sqrtf((float)d);
-    const int e = (bound > 0.f && bound < INFINITY) ? min(max(ilogbf(bound) - 14, -126), 126) : 0;
-    const float down = exp2f((float)-e);
-    if (lane == 0 && cb == 0) a.fscale[row] = a.scale * kLog2eF * exp2f((float)e);
+#pragma unroll 1
+    for (int r = warp; r < nr; r += kPrepThreads / 32) {
+        const int64_t row = r0 + r, slice = row / a.rows_in;
+        const int rr = (int)(row - slice * a.rows_in), b = (int)(slice / a.Hkv), kv = (int)(slice - (int64_t)b * a.Hkv);
+        const int pr = b * a.rows_in + rr;
+        const float bound = rmax[r] * qbound * sqrtf((float)d);
+        const int e = (bound > 0.f && bound < INFINITY) ? min(max(ilogbf(bound) - 14, -126), 126) : 0;
+        const float down = exp2f((float)-e);
+        if (lane == 0 && cb == 0) a.fscale[row] = a.scale * kLog2eF * exp2f((float)e);
+        uint16_t *own = nullptr, *pre = nullptr;
+        if (a.own_frag)
+            own = a.own_frag + frag_row(slice, (a.rows_in + a.row_block - 1) / a.row_block, a.row_block, d, rr);
+        if (a.pre_frag) pre = a.pre_frag + frag_row(kv, a.prefix_blocks, a.row_block, d, pr);
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        const int cc = lane + 32 * k, oc = cb + cc;
-        if (oc >= n) break;
-        const float x = ((red[0][r][cc] + red[1][r][cc]) + (red[2][r][cc] + red[3][r][cc])) *
-                        ((oc < d ? sigma : gamma) * down);
-        if (a.qprep) a.qprep[row * n + oc] = x;
-        if (a.own_frag) put_split(a.own_frag + own_row + place[k], x);
-        if (a.pre_frag) put_split(a.pre_frag + pre_row + place[k], x);
-        if (a.qrows) a.qrows[qrow + prefix_column(d, oc)] = __half_as_ushort(__float2half_rn(x));
+        for (int k = 0; k < 2; ++k) {
+            const int cc = lane + 32 * k, oc = cb + cc;
+            if (oc >= n) break;
+            const float x = ((red[0][r][cc] + red[1][r][cc]) + (red[2][r][cc] + red[3][r][cc])) *
+                            ((oc < d ? sigma : gamma) * down);
+            if (a.qprep) a.qprep[row * n + oc] = x;
+            if (own) put_split(own + place[k], x);
+            if (pre) put_split(pre + place[k], x);
+            if (a.qrows)
+                a.qrows[((int64_t)kv * a.B * a.rows_in + pr) * n + prefix_column(d, oc)] =
+                    __half_as_ushort(__float2half_rn(x));
+        }
     }
 }
 
@@ -375,8 +381,7 @@ __global__ void __launch_bounds__(kPlThreads) ragged_plain_kernel(RaggedArgs a) 
 // ------------------------------------------------------------------ merge and weights
 
 constexpr int kFinThreads = 512;
-constexpr int kMgRows = 8;       // query rows of a merging CTA, two warps each
-constexpr int kMgParts = 8;      // partials of a row on their way at once
+constexpr int kMgParts = 4;      // partials of a warp on their way at once
 constexpr int kWtTokens = 1024;  // tokens of a weighing CTA
 constexpr int kWtRows = 64;      // rows whose normalisers it holds at a time
 
@@ -472,35 +477,38 @@ __global__ void __launch_bounds__(kWtThreads) serve_weigh_kernel(FinishArgs a) {
     weigh_tokens<kWtThreads, true>(a, blockIdx.x, lse);
 }
 
-// Merging CTAs: out = R^T o / l for kMgRows rows.  Two warps a row add its partials, each half of
-// them in the order of the context, rescaled to their largest reference as they come; the rows are
-// then rotated back together, several threads an output.  A row without a token is zero.
-// Latency bound at a few rows: the partials' and R's loads are issued before anything waits.
+// Merging CTAs: out = R^T o / l for kMgRows rows.  16 / kMgRows warps a row add its partials, a share
+// of the list each, in the order of the context and rescaled to their largest reference as they come;
+// the rows are then rotated back together, several threads an output.  A row without a token is
+// zero.  Latency bound at a few rows: the partials' and R's loads are issued before anything waits,
+// and the code is kept short (it is fetched anew by every launch).
+template <int kMgRows>
 __global__ void __launch_bounds__(kFinThreads) serve_finish_kernel(FinishArgs a) {
+    constexpr int kMgWarps = kFinThreads / 32 / kMgRows;
     grid_go();
-    extern __shared__ __align__(16) float osm[];  // [2][d][kMgRows]
-    __shared__ float red[kFinThreads * kMgRows];
-    __shared__ float2 head[2][kMgRows];
+    extern __shared__ __align__(16) float osm[];  // [kMgWarps][d][kMgRows]
+    __shared__ __align__(16) float red[kFinThreads * kMgRows];
+    __shared__ float2 head[kMgWarps][kMgRows];
     if (blockIdx.x >= a.merge_ctas) {
         weigh_tokens<kFinThreads, false>(a, blockIdx.x - a.merge_ctas, red);
         return;
     }
     const int d = a.P.d, ps = partial_stride(d), tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t row0 = (int64_t)(blockIdx.x / a.csplit) * kMgRows;
-    // this thread's column(s) of R^T o and its share of the sum
+    // this thread's column of R^T o (the first of several past 512 columns) and its share of the sum
     const int cw = d / a.csplit, c0 = (int)(blockIdx.x % a.csplit) * cw;
     const int ncol = min(cw, kFinThreads), ks = min(kFinThreads / ncol, d / 4), part = d / ks;
-    const int col = c0 + tid % ncol, i0 = tid / ncol * part;
-    const bool works = tid / ncol < ks;
-    const float *w = a.P.R + (int64_t)i0 * d + col;
+    const int share = tid / ncol, cl = tid - share * ncol, i0 = share * part;
+    const bool works = share < ks;
+    const float *w = a.P.R + (int64_t)i0 * d + c0 + cl;
     float first[32];
 #pragma unroll
     for (int k = 0; k < 32; ++k) first[k] = works && k < part ? w[(int64_t)k * d] : 0.f;
     {
         // where the row's partials are: the preparation, whose lengths this takes, is over (the kernel
         // before lets this one start behind its own wait for it)
-        const int r8 = warp >> 1, half = warp & 1;
-        const int64_t row = row0 + r8;
+        const int r4 = warp / kMgWarps, q = warp % kMgWarps;
+        const int64_t row = row0 + r4;
         Parts g[2] = {{nullptr, 0, 0}, {nullptr, 0, 0}};
         if (row < a.rows) {
             const int slice = (int)(row / a.rows_in), r = (int)(row - (int64_t)slice * a.rows_in);
@@ -515,25 +523,28 @@ __global__ void __launch_bounds__(kFinThreads) serve_finish_kernel(FinishArgs a)
             g[1] = parts_of(a.own, a.own_part, slice, r, ps);
         }
         grid_wait();
-        // the prefix's partials, then the own ones, as one list; this warp's half of it
-        const int all = g[0].n + g[1].n, mid = (all + 1) / 2, p0 = half ? mid : 0, p1 = half ? all : mid;
-        for (int j0 = 0; j0 < d; j0 += 128) {
-            const int j = min(j0 + 4 * lane, d - 4);
-            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        // the prefix's partials, then the own ones, as one list; this warp's share of it
+        const int all = g[0].n + g[1].n, per = (all + kMgWarps - 1) / kMgWarps;
+        const int p0 = min(q * per, all), p1 = min(p0 + per, all);
+        for (int j0 = 0; j0 < d; j0 += 256) {  // two groups of 128 coordinates at a time, four a lane of each
+            const bool two = j0 + 128 < d;
+            const int ja = min(j0 + 4 * lane, d - 4), jb = two ? j0 + 128 + 4 * lane : ja;
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
             float N = -INFINITY, L = 0.f;
+#pragma unroll 1
             for (int p = p0; p < p1; p += kMgParts) {
                 float2 h[kMgParts];
-                float4 o[kMgParts];
+                float4 ox[kMgParts], oy[kMgParts];
 #pragma unroll
                 for (int k = 0; k < kMgParts; ++k) {
-                    h[k] = make_float2(-INFINITY, 0.f);
-                    o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (p + k < p1) {
-                        const Parts &q = p + k < g[0].n ? g[0] : g[1];
-                        const float *at = q.base + (p + k < g[0].n ? p + k : p + k - g[0].n) * q.step;
-                        h[k] = *(const float2 *)at;
-                        o[k] = *(const float4 *)(at + 4 + j);
-                    }
+                    // (past the end: the last partial again, with nothing in it)
+                    const int e = min(p + k, p1 - 1);
+                    const bool pre = e < g[0].n;
+                    const float *at = pre ? g[0].base + e * g[0].step : g[1].base + (e - g[0].n) * g[1].step;
+                    h[k] = *(const float2 *)at;
+                    ox[k] = *(const float4 *)(at + 4 + ja);
+                    oy[k] = *(const float4 *)(at + 4 + jb);
+                    if (p + k >= p1) h[k].x = -INFINITY;
                 }
                 float up = N;
 #pragma unroll
@@ -541,73 +552,87 @@ __global__ void __launch_bounds__(kFinThreads) serve_finish_kernel(FinishArgs a)
                 const float sc = N == -INFINITY ? 0.f : exp2f(N - up);
                 N = up;
                 L *= sc;
-                acc.x *= sc;
-                acc.y *= sc;
-                acc.z *= sc;
-                acc.w *= sc;
+                x = make_float4(x.x * sc, x.y * sc, x.z * sc, x.w * sc);
+                y = make_float4(y.x * sc, y.y * sc, y.z * sc, y.w * sc);
 #pragma unroll
                 for (int k = 0; k < kMgParts; ++k) {
-                    const float f = h[k].x == -INFINITY ? 0.f : exp2f(h[k].x - up);
+                    if (h[k].x == -INFINITY) continue;
+                    const float f = exp2f(h[k].x - up);
                     L = fmaf(f, h[k].y, L);
-                    acc.x = fmaf(f, o[k].x, acc.x);
-                    acc.y = fmaf(f, o[k].y, acc.y);
-                    acc.z = fmaf(f, o[k].z, acc.z);
-                    acc.w = fmaf(f, o[k].w, acc.w);
+                    x = make_float4(fmaf(f, ox[k].x, x.x), fmaf(f, ox[k].y, x.y), fmaf(f, ox[k].z, x.z),
+                                    fmaf(f, ox[k].w, x.w));
+                    y = make_float4(fmaf(f, oy[k].x, y.x), fmaf(f, oy[k].y, y.y), fmaf(f, oy[k].z, y.z),
+                                    fmaf(f, oy[k].w, y.w));
                 }
             }
-            if (j0 + 4 * lane < d) {
-                float *o = osm + (half * d + j) * kMgRows + r8;
-                o[0] = acc.x;
-                o[kMgRows] = acc.y;
-                o[2 * kMgRows] = acc.z;
-                o[3 * kMgRows] = acc.w;
-            }
-            if (j0 == 0 && lane == 0) head[half][r8] = make_float2(N, L);
+            auto put = [&](int j, float4 v) {
+                float *o = osm + ((size_t)q * d + j) * kMgRows + r4;
+                o[0] = v.x;
+                o[kMgRows] = v.y;
+                o[2 * kMgRows] = v.z;
+                o[3 * kMgRows] = v.w;
+            };
+            if (j0 + 4 * lane < d) put(ja, x);
+            if (two) put(jb, y);
+            if (j0 == 0 && lane == 0) head[q][r4] = make_float2(N, L);
         }
     }
     __syncthreads();
-    // the halves of a row together, over the normaliser
+    // the shares of a row together, over the normaliser
     for (int e = tid; e < d * kMgRows; e += kFinThreads) {
         const int r = e % kMgRows;
-        const float2 x = head[0][r], y = head[1][r];
-        const float N = fmaxf(x.x, y.x);
-        const float fx = x.x == -INFINITY ? 0.f : exp2f(x.x - N), fy = y.x == -INFINITY ? 0.f : exp2f(y.x - N);
-        const float L = fx * x.y + fy * y.y, inv = L != 0.f ? 1.f / L : 0.f;
-        osm[e] = (fx * osm[e] + fy * osm[d * kMgRows + e]) * inv;
+        float N = -INFINITY, L = 0.f, v = 0.f;
+#pragma unroll
+        for (int q = 0; q < kMgWarps; ++q) N = fmaxf(N, head[q][r].x);
+#pragma unroll
+        for (int q = 0; q < kMgWarps; ++q) {
+            const float2 h = head[q][r];
+            const float f = h.x == -INFINITY ? 0.f : exp2f(h.x - N);
+            L = fmaf(f, h.y, L);
+            v = fmaf(f, osm[(size_t)q * d * kMgRows + e], v);
+        }
+        osm[e] = L != 0.f ? v / L : 0.f;
         if (a.lse && e < kMgRows && c0 == 0 && row0 + r < a.rows) a.lse[row0 + r] = L == 0.f ? INFINITY : N + log2f(L);
     }
     __syncthreads();
-    for (int c = col; c - col < cw; c += ncol) {  // one column a thread up to 512 of them
-        float acc[kMgRows] = {};
+#pragma unroll 1
+    for (int cc = 0; cc < cw; cc += ncol) {  // once up to 512 columns
+        f2 acc[kMgRows / 2];
+#pragma unroll
+        for (int r = 0; r < kMgRows / 2; ++r) acc[r] = pack2(0.f, 0.f);
         const float4 *o4 = (const float4 *)(osm + i0 * kMgRows);
         auto add = [&](float v, int k) {
-            const float4 x = o4[2 * k], y = o4[2 * k + 1];
-            acc[0] = fmaf(v, x.x, acc[0]);
-            acc[1] = fmaf(v, x.y, acc[1]);
-            acc[2] = fmaf(v, x.z, acc[2]);
-            acc[3] = fmaf(v, x.w, acc[3]);
-            acc[4] = fmaf(v, y.x, acc[4]);
-            acc[5] = fmaf(v, y.y, acc[5]);
-            acc[6] = fmaf(v, y.z, acc[6]);
-            acc[7] = fmaf(v, y.w, acc[7]);
+            const f2 vv = pack2(v, v);
+#pragma unroll
+            for (int r = 0; r < kMgRows / 4; ++r) {
+                const float4 x = o4[k * (kMgRows / 4) + r];
+                acc[2 * r] = fma2(vv, pack2(x.x, x.y), acc[2 * r]);
+                acc[2 * r + 1] = fma2(vv, pack2(x.z, x.w), acc[2 * r + 1]);
+            }
         };
-        if (works && c == col) {
+        if (works) {
+            if (cc == 0) {
 #pragma unroll
-            for (int k = 0; k < 32; ++k)
-                if (k < part) add(first[k], k);
+                for (int k = 0; k < 32; ++k)
+                    if (k < part) add(first[k], k);
+            }
+#pragma unroll 8
+            for (int k = cc == 0 ? 32 : 0; k < part; ++k) add(w[(int64_t)k * d + cc], k);
+#pragma unroll
+            for (int r = 0; r < kMgRows / 4; ++r) {
+                float4 x;
+                unpack2(acc[2 * r], x.x, x.y);
+                unpack2(acc[2 * r + 1], x.z, x.w);
+                *(float4 *)(red + (share * ncol + cl) * kMgRows + 4 * r) = x;
+            }
         }
-#pragma unroll 16
-        for (int k = c == col ? 32 : 0; works && k < part; ++k) add(a.P.R[(int64_t)(i0 + k) * d + c], k);
-#pragma unroll
-        for (int r = 0; r < kMgRows; ++r)
-            if (works) red[(tid / ncol * kMgRows + r) * ncol + tid % ncol] = acc[r];
         __syncthreads();
         for (int e = tid; e < kMgRows * ncol; e += kFinThreads) {
-            const int r = e / ncol, cc = e - r * ncol;
+            const int r = e % kMgRows, c = e / kMgRows;
             float v = 0.f;
-            for (int k = 0; k < ks; ++k) v += red[(k * kMgRows + r) * ncol + cc];
+            for (int k = 0; k < ks; ++k) v += red[k * ncol * kMgRows + e];
             if (row0 + r < a.rows) {
-                const int64_t at = (row0 + r) * d + c0 + (c - col) + cc;
+                const int64_t at = (row0 + r) * d + c0 + cc + c;
                 if (a.dtype == TQ_F16) ((__half *)a.out)[at] = __float2half_rn(v);
                 else if (a.dtype == TQ_BF16) ((__nv_bfloat16 *)a.out)[at] = __float2bfloat16_rn(v);
                 else ((float *)a.out)[at] = v;
@@ -690,9 +715,9 @@ cudaError_t launch_ragged_mma(const RaggedArgs &own, const RaggedArgs &prefix, c
 
 namespace {
 // CTAs among which the stages of a cache are divided: enough to fill the GPU once together with
-// the row blocks, and no more than there are fours of stages (a CTA's warps take one each).
+// the row blocks, and no more than there are eights of counted stages.
 int division(int64_t slices, int64_t cap, int64_t row_blocks, int per_sm) {
-    const int64_t most = slices * ((cap + 4 * kStage - 1) / (4 * kStage));
+    const int64_t most = slices * ((counted_stages(cap) + 7) / 8);
     int64_t want = ((int64_t)kSms * per_sm + row_blocks - 1) / row_blocks;
     if (want > most) want = most;
     return (int)(want < 1 ? 1 : want);
@@ -771,8 +796,14 @@ cudaError_t launch_serve(const ServeCall &call, const ServePlan &plan, void *scr
     pa.len_own = (int32_t *)(base + plan.lens);
     pa.cum_own = (int64_t *)(base + plan.cum);
     pa.dev_status = call.dev_status;
-    const int64_t prep_ctas = (call.rows + kPrepRows - 1) / kPrepRows * ((P.d + P.m + kPrepCols - 1) / kPrepCols) + 1;
-    serve_prep_kernel<<<(unsigned)prep_ctas, kPrepThreads, sizeof(float) * kPrepRows * P.d, s>>>(pa);
+    // rows that fill the GPU several times over: twice as many a CTA, for half the reads of R
+    const int64_t cols = (P.d + P.m + kPrepCols - 1) / kPrepCols;
+    const bool many = call.rows * cols >= 8 * 4 * kSms && P.d <= 256;
+    const int prep_rows = many ? 16 : 8;
+    const unsigned prep_ctas = (unsigned)((call.rows + prep_rows - 1) / prep_rows * cols + 1);
+    const size_t prep_smem = sizeof(float) * prep_rows * P.d;
+    if (many) serve_prep_kernel<16><<<prep_ctas, kPrepThreads, prep_smem, s>>>(pa);
+    else serve_prep_kernel<8><<<prep_ctas, kPrepThreads, prep_smem, s>>>(pa);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
 
@@ -830,8 +861,10 @@ cudaError_t launch_serve(const ServeCall &call, const ServePlan &plan, void *scr
     fa.Hkv = call.Hkv;
     fa.dtype = call.dtype;
     fa.out = call.out;
-    // few rows: the columns of a block of rows go to several CTAs, which merge the same partials each
-    const int64_t blocks = (call.rows + kMgRows - 1) / kMgRows;
+    // A CTA fills an SM: blocks of few rows, as long as they make one wave.  Fewer rows than that: the
+    // columns of a block go to several CTAs, which merge the same partials each.
+    const int mg_rows = call.rows <= 4 * kSms ? 4 : call.rows <= 8 * kSms ? 8 : 16;
+    const int64_t blocks = (call.rows + mg_rows - 1) / mg_rows;
     fa.csplit = 1;
     while (fa.csplit < P.d / 64 && blocks * fa.csplit * 2 <= kSms) fa.csplit *= 2;
     const int64_t merge = blocks * fa.csplit;
@@ -843,16 +876,19 @@ cudaError_t launch_serve(const ServeCall &call, const ServePlan &plan, void *scr
         weigh = (int64_t)fa.chunks * call.B * call.Hkv;
     }
     fa.merge_ctas = (unsigned)merge;
-    const size_t fin_smem = 2 * sizeof(float) * kMgRows * P.d;
-    if (fin_smem >= 32 * 1024) {  // with the static arrays above what is allowed without asking
-        e = allow_smem((const void *)serve_finish_kernel, 2 * sizeof(float) * kMgRows * kMaxDim);
+    const auto finish = mg_rows == 4   ? serve_finish_kernel<4>
+                        : mg_rows == 8 ? serve_finish_kernel<8>
+                                       : serve_finish_kernel<16>;
+    const size_t fin_smem = sizeof(float) * (kFinThreads / 32) * P.d;
+    if (fin_smem >= 8 * 1024) {  // with the static arrays it can be above what is allowed without asking
+        e = allow_smem((const void *)finish, sizeof(float) * (kFinThreads / 32) * kMaxDim);
         if (e != cudaSuccess) return e;
     }
     // Few weighing CTAs ride along with the merging ones; many get a launch of their own, where more of
     // them fit an SM (8 against 1: 11 against 50 us for 2048 of them).
     const bool along = weigh <= kSms;
     if (!along) fa.lse = (float *)(base + plan.lse);
-    e = launch_after(serve_finish_kernel, (unsigned)(merge + (along ? weigh : 0)), kFinThreads, fin_smem, s, fa);
+    e = launch_after(finish, (unsigned)(merge + (along ? weigh : 0)), kFinThreads, fin_smem, s, fa);
     if (e != cudaSuccess || along) return e;
     return launch_after(serve_weigh_kernel, (unsigned)weigh, kWtThreads, 0, s, fa);
 }
