@@ -7,47 +7,53 @@
 // above every number; the last `recent` tokens are 0xFFFFFFFF.  The kept set is the budget largest
 // (key, smaller slot first), found by a radix selection: the threshold key's digits from the top,
 // each from a histogram of the keys that match the digits before.
+#include <type_traits>
+
 #include "tq_common.cuh"
 #include "tq_evict.cuh"
 #include "tq_launch.cuh"
+#include "tq_serve.cuh"
 
 namespace tq {
 
 namespace {
 
-constexpr int kSelThreads = 1024;
+constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
+constexpr int kAtOnce = 8;  // weights a thread has on their way at once
+constexpr size_t kHeldMax = 200 * 1024;  // bytes of keys that a CTA can hold
 
+// (The addition makes -0 a 0 and any NaN the positive one with all other bits set.)
 __device__ __forceinline__ uint32_t weight_key(float w) {
-    if (w != w) return 0xFFFFFFFEu;
-    const uint32_t u = __float_as_uint(w + 0.f);
-    return (u & 0x80000000u) ? ~u : u | 0x80000000u;
+    const int32_t u = __float_as_int(w + 0.f);
+    return min((uint32_t)u ^ ((uint32_t)(u >> 31) | 0x80000000u), 0xFFFFFFFEu);
 }
 
-// This warp's exclusive prefix of the warps' sums, and their total.
-__device__ __forceinline__ uint32_t before_warp(const uint32_t *wsum, int warp, int lane, uint32_t *all) {
-    const uint32_t v = wsum[lane];
-    uint32_t s = v;
-    for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t y = __shfl_up_sync(kFull, s, o);
-        if (lane >= o) s += y;
-    }
-    *all = __shfl_sync(kFull, s, 31);
-    return __shfl_sync(kFull, s - v, warp);
+// One more in a bin of shared memory, if `yes`: one predicated instruction, no branch.
+__device__ __forceinline__ void count_if(bool yes, uint32_t *bin) {
+    asm volatile(
+        "{ .reg .pred p; setp.ne.u32 p, %0, 0;\n\t"
+        "@p red.shared.add.u32 [%1], 1; }" ::"r"((uint32_t)yes),
+        "r"((uint32_t)__cvta_generic_to_shared(bin))
+        : "memory");
 }
 
-// One CTA per slice; a thread holds up to KPT keys in registers, loaded at once, so that the slice is
-// read once while it has at most KPT x 1024 tokens (longer ones in rounds, read again from L2 by each
-// step).  Three histograms in shared memory find the threshold; then every warp's counts of each group of 32
-// keys are scanned together, which gives each key its place.
-template <int KPT>
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictCall c) {
-    constexpr int ROUND = KPT * kSelThreads;
+template <uint32_t N>
+using Step = std::integral_constant<uint32_t, N>;
+
+// One CTA per slice, two an SM where the keys leave room.  HELD: the keys wait in shared memory between
+// the steps; otherwise each step reads the weights again, mostly from L2.  Three histograms in shared
+// memory find the threshold; then every warp takes a run of consecutive slots, counts what it keeps,
+// and, with the counts of the warps before it, writes the kept slots in their order.
+// Bound by instructions and the latency of the five steps: 256 slices of 4352 tokens 12 us, of 26000
+// tokens 40 us (keys in registers, 1024 threads a slice: 18 and 45 us).
+template <bool HELD>
+__global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(EvictCall c) {
     grid_go();
-    __shared__ uint32_t hist[kBins];
-    __shared__ uint32_t cnt[KPT * kSelWarps];  // [group of a round][warp]: keys above | keys equal << 16
-    __shared__ uint32_t wsum[kSelWarps];
+    extern __shared__ uint32_t held[];  // HELD: [t_cap]
+    __shared__ __align__(16) uint32_t hist[kBins];
+    __shared__ uint32_t sums[2][kSelWarps];
     __shared__ uint32_t s_digit, s_rank;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int slice = blockIdx.x, b = slice / c.Hkv;
@@ -56,64 +62,93 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictCall c) 
         if (tid == 0 && c.dev_status) *c.dev_status = TQ_ERR_INVALID_ARG;
         len = len < 0 ? 0 : c.t_cap;
     }
-    const int n = (int)len, budget = (int)c.budget;
-    const int keep = n < budget ? n : budget;
+    const uint32_t n = (uint32_t)len, budget = (uint32_t)c.budget;
+    const uint32_t keep = n < budget ? n : budget;
     int32_t *kept = c.kept + (int64_t)slice * budget;
     if (tid == 0) {
-        c.counts[slice] = keep;
-        if (slice == b * c.Hkv) c.out_lens[b] = keep;
+        c.counts[slice] = (int32_t)keep;
+        if (slice == b * c.Hkv) c.out_lens[b] = (int32_t)keep;
     }
     if (n <= budget) {
-        for (int t = tid; t < n; t += kSelThreads) kept[t] = t;
+        for (uint32_t t = tid; t < n; t += kSelThreads) kept[t] = (int32_t)t;
         return;
     }
     const float *w = (const float *)c.src[6] + (int64_t)slice * c.t_cap;
-    const int safe = n - (int)c.recent;  // slots from here on are kept
-    const int rounds = (n - 1) / ROUND + 1;
-    uint32_t key[KPT];
-    auto load = [&](int round) {
-        const int t0 = round * ROUND + tid;
-        float v[KPT];
+    const uint32_t safe = n - (uint32_t)c.recent;  // slots from here on are kept
+    // the keys of slots t, t + STEP, ...: `whole`, none of them past `safe` or the end
+    auto keys_at = [&](auto step, bool again, bool whole, uint32_t t, uint32_t end, uint32_t(&x)[kAtOnce]) {
+        constexpr uint32_t STEP = decltype(step)::value;
+        const float *p = w + t;
+        const uint32_t *q = held + t;
 #pragma unroll
-        for (int i = 0; i < KPT; ++i) v[i] = t0 + i * kSelThreads < n ? w[t0 + i * kSelThreads] : 0.f;
+        for (int i = 0; i < kAtOnce; ++i)
+            if (whole || t + i * STEP < end) x[i] = HELD && again ? q[i * STEP] : __float_as_uint(p[i * STEP]);
+        if (HELD && again) return;
 #pragma unroll
-        for (int i = 0; i < KPT; ++i) key[i] = t0 + i * kSelThreads >= safe ? 0xFFFFFFFFu : weight_key(v[i]);
+        for (int i = 0; i < kAtOnce; ++i)
+            x[i] = !whole && t + i * STEP >= safe ? 0xFFFFFFFFu : weight_key(__uint_as_float(x[i]));
     };
-    load(0);
+    // f(key, slot) for the slots t, t + STEP, ... below end, kAtOnce loads at a time
+    auto sweep = [&](auto step, bool again, uint32_t t, uint32_t end, auto f) {
+        constexpr uint32_t STEP = decltype(step)::value;
+        const uint32_t plain = HELD && again ? end : min(end, safe);
+        uint32_t x[kAtOnce] = {};
+        for (; t + (kAtOnce - 1) * STEP < plain; t += kAtOnce * STEP) {
+            keys_at(step, again, true, t, end, x);
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i) f(x[i], t + i * STEP);
+        }
+        for (; t < end; t += kAtOnce * STEP) {
+            keys_at(step, again, false, t, end, x);
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i)
+                if (t + i * STEP < end) f(x[i], t + i * STEP);
+        }
+    };
+    const Step<kSelThreads> all_threads;
+    const Step<32> one_warp;
     // the threshold: the keep-th largest key, found 11, 11 and 10 bits at a time
-    uint32_t prefix = 0, mask = 0, rank = (uint32_t)keep;  // the rank-th largest of the keys that match
+    uint32_t prefix = 0, mask = 0, rank = keep;  // the rank-th largest of the keys that match
 #pragma unroll 1
     for (int pass = 0; pass < 3; ++pass) {
         const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
         const uint32_t dm = pass < 2 ? 2047u : 1023u;
-        for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
+        *(uint4 *)(hist + 4 * tid) = make_uint4(0u, 0u, 0u, 0u);
         __syncthreads();
-        for (int r = 0; r < rounds; ++r) {
-            if (rounds > 1) load(r);
-            const int t0 = r * ROUND + tid;
-#pragma unroll
-            for (int i = 0; i < KPT; ++i)
-                if (t0 + i * kSelThreads < n && (key[i] & mask) == prefix) atomicAdd(&hist[(key[i] >> shift) & dm], 1u);
+        if (pass == 0) {
+            sweep(all_threads, false, tid, n, [&](uint32_t key, uint32_t s) {
+                if (HELD) held[s] = key;
+                atomicAdd(&hist[key >> 21], 1u);
+            });
+        } else {
+            sweep(all_threads, true, tid, n, [&](uint32_t key, uint32_t) {
+                count_if((key & mask) == prefix, &hist[(key >> shift) & dm]);
+            });
         }
         __syncthreads();
-        // suffix sums over the bins, two a thread, from the top: thread 0 takes the highest two
-        const int hi = kBins - 1 - 2 * tid;
-        const uint32_t h1 = hist[hi], h0 = hist[hi - 1];
-        uint32_t x = h1 + h0;
+        // suffix sums over the bins, four a thread, from the top: thread 0 takes the highest four
+        const uint32_t low = kBins - 4 - 4 * tid;
+        const uint4 h = *(const uint4 *)(hist + low);
+        const uint32_t mine = h.x + h.y + h.z + h.w;
+        uint32_t x = mine;
         for (int o = 1; o < 32; o <<= 1) {
             const uint32_t y = __shfl_up_sync(kFull, x, o);
             if (lane >= o) x += y;
         }
-        if (lane == 31) wsum[warp] = x;
+        if (lane == 31) sums[0][warp] = x;
         __syncthreads();
-        uint32_t all;
-        const uint32_t above = x - (h1 + h0) + before_warp(wsum, warp, lane, &all);
-        if (above < rank && rank <= above + h1) {
-            s_digit = (uint32_t)hi;
-            s_rank = rank - above;
-        } else if (above + h1 < rank && rank <= above + h1 + h0) {
-            s_digit = (uint32_t)hi - 1;
-            s_rank = rank - above - h1;
+        uint32_t above = x - mine;
+        for (int k = 0; k < warp; ++k) above += sums[0][k];
+        if (above < rank && rank <= above + mine) {
+            const uint32_t hs[4] = {h.w, h.z, h.y, h.x};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (above < rank && rank <= above + hs[k]) {
+                    s_digit = low + 3 - k;
+                    s_rank = rank - above;
+                }
+                above += hs[k];
+            }
         }
         __syncthreads();
         prefix |= s_digit << shift;
@@ -121,47 +156,43 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictCall c) 
         rank = s_rank;
     }
     // kept: keys above the threshold, and the first `rank` slots whose key equals it
-    uint32_t gt_before = 0, eq_before = 0;
-    for (int r = 0; r < rounds; ++r) {
-        if (rounds > 1) load(r);
-        const int t0 = r * ROUND + tid;
-        uint32_t gt[KPT], eq[KPT];
+    const uint32_t run = ((n + 31) / 32 + kSelWarps - 1) / kSelWarps * 32;  // slots of a warp
+    const uint32_t first = min(warp * run, n), last = n - first < run ? n : first + run;
+    uint32_t gt = 0, eq = 0;
+    sweep(one_warp, true, first + lane, last, [&](uint32_t key, uint32_t) {
+        gt += key > prefix;
+        eq += key == prefix;
+    });
+    gt = __reduce_add_sync(kFull, gt);
+    eq = __reduce_add_sync(kFull, eq);
+    if (lane == 0) sums[0][warp] = gt, sums[1][warp] = eq;
+    __syncthreads();
+    uint32_t ngt = 0, neq = 0;  // above and equal in the slots before
+    for (int k = 0; k < warp; ++k) ngt += sums[0][k], neq += sums[1][k];
+    const uint32_t below = (1u << lane) - 1u;
+    int32_t *at = kept + ngt + min(neq, rank);
+    auto write = [&](bool whole, uint32_t t) {
+        uint32_t x[kAtOnce] = {};
+        keys_at(one_warp, true, whole, t + lane, last, x);
 #pragma unroll
-        for (int i = 0; i < KPT; ++i) {
-            const bool there = t0 + i * kSelThreads < n;
-            gt[i] = __ballot_sync(kFull, there && key[i] > prefix);
-            eq[i] = __ballot_sync(kFull, there && key[i] == prefix);
-            if (lane == 0) cnt[i * kSelWarps + warp] = __popc(gt[i]) | ((uint32_t)__popc(eq[i]) << 16);
-        }
-        __syncthreads();
-        // exclusive prefix sums of the counts in slot order, KPT a thread in the first 32 warps' lanes
-        uint32_t all = 0;
-        {
-            const uint32_t x = tid < KPT * kSelWarps ? cnt[tid] : 0u;
-            uint32_t s = x;
-            for (int o = 1; o < 32; o <<= 1) {
-                const uint32_t y = __shfl_up_sync(kFull, s, o);
-                if (lane >= o) s += y;
+        for (int i = 0; i < kAtOnce; ++i) {
+            const uint32_t s = t + 32 * i + lane;
+            const bool there = whole || s < last;
+            bool keeps = there && x[i] > prefix;
+            const bool equal = there && x[i] == prefix;
+            const uint32_t es = __ballot_sync(kFull, equal);
+            if (es != 0) {
+                keeps |= equal && neq + __popc(es & below) < rank;
+                neq += __popc(es);
             }
-            if (lane == 31) wsum[warp] = s;
-            __syncthreads();
-            const uint32_t off = before_warp(wsum, warp, lane, &all);
-            if (tid < KPT * kSelWarps) cnt[tid] = off + s - x;
+            const uint32_t ks = __ballot_sync(kFull, keeps);
+            if (keeps) at[__popc(ks & below)] = (int32_t)s;
+            at += __popc(ks);
         }
-        __syncthreads();
-        const uint32_t below = (1u << lane) - 1u;
-#pragma unroll
-        for (int i = 0; i < KPT; ++i) {
-            const uint32_t base = cnt[i * kSelWarps + warp];
-            const uint32_t ngt = gt_before + (base & 0xFFFFu) + __popc(gt[i] & below);
-            const uint32_t neq = eq_before + (base >> 16) + __popc(eq[i] & below);
-            if (((gt[i] >> lane) & 1u) || (((eq[i] >> lane) & 1u) && neq < rank))
-                kept[ngt + min(neq, rank)] = t0 + i * kSelThreads;
-        }
-        gt_before += all & 0xFFFFu;
-        eq_before += all >> 16;
-        __syncthreads();
-    }
+    };
+    uint32_t t = first;
+    for (const uint32_t plain = HELD ? last : min(last, safe); t + 32 * kAtOnce <= plain; t += 32 * kAtOnce) write(true, t);
+    for (; t < last; t += 32 * kAtOnce) write(false, t);
 }
 
 constexpr int kCopyThreads = 256;
@@ -197,7 +228,9 @@ __device__ __forceinline__ void copy_wide(const EvictCall &c, int a, int64_t src
 }
 
 // kCopySlots kept records of one slice per CTA, a thread a record for the norms and weights, and the
-// widest words that every record is aligned to for the packed arrays.  Bound by the bytes moved.
+// widest words that every record is aligned to for the packed arrays.  Bound by DRAM: for one token
+// kept of three (256 slices, 8192 kept of 26000) 102 us, in which it reads 505 MB for the 174 MB that
+// are kept, since DRAM gives 64 bytes for a record of 2 to 48, and writes 174 MB: 6.7 TB/s.
 __global__ void __launch_bounds__(kCopyThreads) evict_copy_kernel(EvictCall c, int chunks) {
     static_assert(kCopySlots == kCopyThreads, "a thread a record");
     __shared__ int32_t idx[kCopySlots];
@@ -225,20 +258,21 @@ __global__ void __launch_bounds__(kCopyThreads) evict_copy_kernel(EvictCall c, i
     copy_wide(c, 1, src0, dst0, idx, cnt, tid);
 }
 
-template <int KPT>
-cudaError_t launch_select(const EvictCall &c, cudaStream_t s) {
-    evict_select_kernel<KPT><<<(unsigned)(c.B * c.Hkv), kSelThreads, 0, s>>>(c);
-    return cudaGetLastError();
-}
-
 }  // namespace
 
 cudaError_t launch_evict(const EvictCall &c, cudaStream_t s) {
-    // as few keys a thread as hold the longest slice in one round
-    const cudaError_t e = c.t_cap <= 2 * kSelThreads    ? launch_select<2>(c, s)
-                          : c.t_cap <= 8 * kSelThreads  ? launch_select<8>(c, s)
-                          : c.t_cap <= 16 * kSelThreads ? launch_select<16>(c, s)
-                                                        : launch_select<32>(c, s);
+    // keys wait in shared memory wherever they fit (256 slices, read again against held: 53.3 against
+    // 51.3 us for 4352 tokens each, 147.3 against 147.0 us for 26000, the copy included)
+    const int64_t slices = c.B * (int64_t)c.Hkv;
+    const size_t held = sizeof(uint32_t) * (size_t)c.t_cap;
+    if (held <= kHeldMax) {
+        const cudaError_t e = allow_smem((const void *)evict_select_kernel<true>, kHeldMax);
+        if (e != cudaSuccess) return e;
+        evict_select_kernel<true><<<(unsigned)slices, kSelThreads, held, s>>>(c);
+    } else {
+        evict_select_kernel<false><<<(unsigned)slices, kSelThreads, 0, s>>>(c);
+    }
+    const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     const int chunks = (int)evict_chunks(c.budget);
     return launch_after(evict_copy_kernel, (unsigned)(chunks * c.B * c.Hkv), kCopyThreads, 0, s, c, chunks);

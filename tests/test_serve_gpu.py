@@ -420,6 +420,21 @@ def test_evict_one_long_slice(tq):
     run_evict(tq, w, [200_003], 100_001, 777, 100_001, d=32, bits=2)
 
 
+@pytest.mark.parametrize("cap", [24_577, 51_201])
+def test_evict_many_long_slices(tq, cap):
+    rng = np.random.default_rng(cap)
+    w = rng.integers(0, 200, (50, 3, cap)).astype(np.float32)  # ties everywhere
+    lens = rng.integers(0, cap + 1, 50)
+    lens[:4] = cap, 0, 1, 300
+    run_evict(tq, w, lens, 300, 20, 301, d=32, bits=2)
+
+
+@pytest.mark.parametrize("cap", [51_200, 51_201])  # the longest slice held on chip, and one more
+def test_evict_few_long_slices(tq, cap):
+    w = np.random.default_rng(cap).standard_normal((1, 3, cap)).astype(np.float32)
+    run_evict(tq, w, [cap], 20_000, 20_000 - 1, 20_000, d=32, bits=2)
+
+
 # ------------------------------------------------------------------- together
 
 def test_a_generation_with_a_shared_prompt_and_a_bounded_cache(tq):
