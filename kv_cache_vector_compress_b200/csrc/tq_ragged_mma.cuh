@@ -545,13 +545,10 @@ cudaError_t launch_dim(const RaggedPair &a, bool f32, int row_block, cudaStream_
 
 template <int D, int KB>
 cudaError_t launch_bits(const RaggedPair &a, bool f32, int row_block, cudaStream_t s) {
-    if (f32) {
-        if constexpr (D < 256) {
-            if (row_block == 8) return launch_one<D, KB, 2, true>(a, s);
-        }
-        return launch_one<D, KB, 1, true>(a, s);
+    if constexpr (D < 256) {
+        if (row_block == 8) return f32 ? launch_one<D, KB, 2, true>(a, s) : launch_one<D, KB, 2, false>(a, s);
     }
-    return row_block == 8 ? launch_one<D, KB, 2, false>(a, s) : launch_one<D, KB, 1, false>(a, s);
+    return f32 ? launch_one<D, KB, 1, true>(a, s) : launch_one<D, KB, 1, false>(a, s);
 }
 
 #define TQ_RAGGED_DIM(D)                                                                              \

@@ -687,13 +687,17 @@ bool ragged_mma_supported(const Prepared &P) {
            P.vbeta == P.kbeta + 1;
 }
 
-// Eight rows a CTA when there are more than four, but for 32-bit results of 256 coordinates, whose
-// accumulators would not fit the registers.
-int ragged_mma_rows(const Prepared &P, bool f32, int64_t rows) {
-    return rows <= 4 || (f32 && P.d >= 256) ? 4 : 8;
-}
-
 int ragged_mma_ctas_per_sm(const Prepared &P) { return P.d >= 256 ? 3 : 4; }
+
+// A CTA takes eight rows where that saves decoding worth more than the CTAs it costs: more than eight
+// rows, or more than four over at least twelve stages for every CTA that fits the GPU.  Blocks of
+// eight against four for 8 rows a slice of 16-bit queries at d = 128, in us: 8 slices of 1000 tokens
+// 20.6 / 18.5, 16 slices of 8000 41.2 / 36.9, 64 slices of 8000 71.8 / 80.0.  At d = 256 four are
+// always faster (30.8 / 24.8, 69 / 61, 161 / 152): eight rows' accumulators leave few registers.
+int ragged_mma_rows(const Prepared &P, int64_t rows, int64_t stages) {
+    if (P.d >= 256 || rows <= 4) return 4;
+    return rows > 8 || stages >= 12 * kSms * ragged_mma_ctas_per_sm(P) ? 8 : 4;
+}
 
 cudaError_t launch_ragged_mma(const RaggedArgs &own, const RaggedArgs &prefix, const ServePlan &plan, bool f32,
                               cudaStream_t s) {
@@ -715,9 +719,10 @@ cudaError_t launch_ragged_mma(const RaggedArgs &own, const RaggedArgs &prefix, c
 
 namespace {
 // CTAs among which the stages of a cache are divided: enough to fill the GPU once together with
-// the row blocks, and no more than there are eights of counted stages.
+// the row blocks, and no more than there are fours of counted stages, one for each warp of a CTA
+// (eights: 16.4 us instead of 14.4 for 4 slices of 200 tokens, 18.5 instead of 17.9 for 2 of 4000).
 int division(int64_t slices, int64_t cap, int64_t row_blocks, int per_sm) {
-    const int64_t most = slices * ((counted_stages(cap) + 7) / 8);
+    const int64_t most = slices * ((counted_stages(cap) + 3) / 4);
     int64_t want = ((int64_t)kSms * per_sm + row_blocks - 1) / row_blocks;
     if (want > most) want = most;
     return (int)(want < 1 ? 1 : want);
@@ -737,7 +742,11 @@ ServePlan plan_serve(const Prepared &P, tq_dtype dtype, int B, int Hq, int Hkv, 
     // many 16-bit rows on one prefix: the many-row kernel
     const bool tc = p.fast && !f32 && t_prefix > 0 && (int64_t)B * R > 8;
     // the ragged kernel takes both caches in one launch, in blocks of the larger number of rows
-    if (p.fast) p.row_block = ragged_mma_rows(P, f32, t_prefix > 0 && !tc ? (int64_t)B * R : R);
+    if (p.fast) {
+        const bool pre = t_prefix > 0 && !tc;
+        const int64_t stages = (int64_t)B * Hkv * counted_stages(t_cap) + (pre ? Hkv * counted_stages(t_prefix) : 0);
+        p.row_block = ragged_mma_rows(P, pre ? (int64_t)B * R : R, stages);
+    }
     if (t_cap > 0) p.own_ctas = division((int64_t)B * Hkv, t_cap, (R + p.row_block - 1) / p.row_block, per_sm);
     if (tc) p.tc = prefix_split(P.d, Hkv, (int64_t)B * R, t_prefix);
     else if (t_prefix > 0)

@@ -220,7 +220,7 @@ struct RaggedArgs {
 };
 cudaError_t launch_ragged_plain(const RaggedArgs &a, cudaStream_t s);
 bool ragged_mma_supported(const Prepared &P);
-int ragged_mma_rows(const Prepared &P, bool f32, int64_t rows);  // the row block for so many rows a slice
+int ragged_mma_rows(const Prepared &P, int64_t rows, int64_t stages);  // the row block for so many rows a slice
 int ragged_mma_ctas_per_sm(const Prepared &P);
 // One launch for the own caches and the prefix (those that the plan gives CTAs).
 struct RaggedPair {
