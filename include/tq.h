@@ -367,8 +367,9 @@ tq_status tq_attend_static(const tq_params *p, const float *q, int B, int Hq, in
  *   scale    : as tq_attend
  *   out      : device [B, Hq, Nq, dim] of dtype
  *   scratch  : tq_attend_shared_scratch_bytes(...) bytes; calls that share it must not overlap
- * Precision: with TQ_F32 the products keep 32 bits.  With the 16-bit types the operands of a
- * product are rounded to 16 bits (relative 2^-11) and sums, maxima and normalisers are in 32.
+ * Precision: sums, maxima and normalisers are in 32 bits.  With TQ_F32 every operand of a product
+ * keeps 20 bits or more (fp16 pairs hi + lo; fp32 where there is no tensor-core kernel).  With the
+ * 16-bit types operands are rounded to fp16 (relative 2^-11).
  * TQ_ERR_UNSUPPORTED when t_prefix or t_cap exceeds 2^31 - 1024 or B * Hq * Nq exceeds 262140.
  */
 size_t tq_attend_shared_scratch_bytes(const tq_params *p, tq_dtype dtype, int B, int Hq, int Hkv, int Nq,
@@ -389,10 +390,10 @@ tq_status tq_attend_shared(const tq_params *p, const void *q, tq_dtype dtype, in
  *   weights[b, h, t] +=  sum over the Hq/Hkv * Nq query rows of KV head h of softmax_t(scale * s_t),
  *                        for t < lens[b]; entries behind are left as they are
  *   weights : device fp32 [B, Hkv, t_cap]
- * The other arguments are those of tq_attend_shared; t_cap >= 1.  In the scores
- * the query rows keep 22 bits whatever dtype is, and the key centroids 20 or more; with the 16-bit
- * types, centroids of 4-bit parameter sets are off by 3.1e-5 of themselves at most.  The rows are added in ascending order: results are bit-identical
- * run to run.
+ * The other arguments are those of tq_attend_shared; t_cap >= 1.  In the scores the query rows keep
+ * 22 bits whatever dtype is, and the key centroids 20 or more; with the 16-bit types, centroids of
+ * 4-bit parameter sets are off by 3.1e-5 of themselves at most.  The rows are added in ascending
+ * order: results are bit-identical run to run.
  *   scratch : tq_attend_weigh_scratch_bytes(...) bytes, among them 4 for each (query row, slot)
  */
 size_t tq_attend_weigh_scratch_bytes(const tq_params *p, tq_dtype dtype, int B, int Hq, int Hkv, int Nq,

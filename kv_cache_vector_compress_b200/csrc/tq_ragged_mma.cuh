@@ -11,10 +11,16 @@
 // codes are interleaved nibble by nibble.
 //
 // Precision.  A query row is split in two fp16 numbers, hi + lo, in two columns of B, whose sums are
-// added: the scores keep 22 bits of Q, and the key operands are exact to 2^-21 for 1 and 2
-// bits (ServeTables: a well chosen scale).  For 3 bits they are off by 3e-5 at most, 8e-6 on average,
-// with that scale; F32 adds a second table, which costs as much again as the first.  Value sums: fp16 weights and
-// centroids for 16-bit outputs; F32 splits both.
+// added: the scores keep 22 bits of Q, and the key operands are exact to 2^-21 for 1 and 2 bits
+// (ServeTables: a well chosen scale).  For 3 bits they are off by 3e-5 at most, 8e-6 on average, with
+// that scale; F32 adds a second table, which costs as much again as the first.  Value sums: fp16
+// weights and centroids for 16-bit outputs; F32 splits both.
+//
+// Bound by decoding: its byte permutations and logic run on the ALU pipe, which takes an instruction
+// every other cycle and is 63 to 65% busy; DRAM and the matrix instructions are far from theirs.
+// 256 slices of 4096 tokens on average, 4 rows, d = 128, 3 bits: 62 us, 1.7 TB/s of records and
+// weights; 32 slices of 65536, d = 256, 4 bits: 300 us, 1.8 TB/s.  More CTAs an SM with fewer
+// registers each were slower.
 #pragma once
 
 #include <float.h>
@@ -119,7 +125,8 @@ __device__ __forceinline__ float lg2(float x) {
 // The reference N of a row moves only when some y exceeds it by more than 8: then the accumulators
 // are rescaled (rare after the first stages), so that the usual path has no reduction over lanes.
 template <int D, int KB, int NT, bool F32>
-__global__ void __launch_bounds__(NW * 32, D >= 256 ? 3 : F32 || NT > 1 ? 3 : 4) ragged_mma_kernel(const __grid_constant__ RaggedPair pair) {
+__global__ void __launch_bounds__(NW * 32, D >= 256 || F32 || NT > 1 ? 3 : 4)
+    ragged_mma_kernel(const __grid_constant__ RaggedPair pair) {
     using C = Cfg<D, KB, NT, F32>;
     constexpr int VB = C::VB, VN = VB < 3 ? VB : 3;
     extern __shared__ __align__(16) uint8_t smem[];
@@ -554,7 +561,7 @@ cudaError_t launch_bits(const RaggedPair &a, bool f32, int row_block, cudaStream
 #define TQ_RAGGED_DIM(D)                                                                              \
     template <>                                                                                       \
     cudaError_t launch_dim<D>(const RaggedPair &a, bool f32, int row_block, cudaStream_t s) {         \
-        switch (a.a[0].P.kbeta) {                                                                          \
+        switch (a.a[0].P.kbeta) {                                                                     \
             case 1: return launch_bits<D, 1>(a, f32, row_block, s);                                   \
             case 2: return launch_bits<D, 2>(a, f32, row_block, s);                                   \
             case 3: return launch_bits<D, 3>(a, f32, row_block, s);                                   \

@@ -22,7 +22,7 @@
 
 namespace tq {
 
-constexpr int kSms = 148;     // grid sizing (fixed so that scratch sizes do not vary)
+constexpr int kSms = 148;        // grid sizing (fixed so that scratch sizes do not vary)
 constexpr int kStage = 32;       // tokens of one copy stage: the unit in which contexts are divided
 constexpr float kMinNorm = 5.9604644775390625e-8f;  // 2^-24
 constexpr float kLog2eF = 1.4426950408889634f;
@@ -54,8 +54,9 @@ __device__ __forceinline__ int64_t ragged_row(const RaggedCache &c, int slice, i
 // The W stages of all slices, in order, are divided evenly among G = min(ctas, W) CTAs, so that none
 // of these is without work; CTA i takes stages [i W / G, (i + 1) W / G) and so a piece of one or
 // more slices.  A slice that is not empty counts kPieceCost stages more than it has, in front, for
-// what a piece costs besides its stages (its first loads, its partial result).  Slice s's piece in CTA i has the partial number i + s: from one piece to the next
-// either i or s grows, so no two pieces share one.
+// what a piece costs besides its stages (its first loads, its partial result).  Slice s's piece in
+// CTA i has the partial number i + s: from one piece to the next either i or s grows, so no two
+// pieces share one.
 constexpr int kPieceCost = 3;
 __host__ __device__ constexpr int64_t counted_stages(int64_t tokens) {
     return tokens > 0 ? (tokens + kStage - 1) / kStage + kPieceCost : 0;
@@ -63,9 +64,9 @@ __host__ __device__ constexpr int64_t counted_stages(int64_t tokens) {
 
 struct Piece {
     int slice;
-    int64_t s0, s1;  // stages of the slice (there may be none)
+    int64_t s0, s1;   // stages of the slice (there may be none)
     int64_t counted;  // what the piece counts in the division
-    int len;         // tokens of the slice
+    int len;          // tokens of the slice
 };
 
 __device__ __forceinline__ int64_t ragged_total(const RaggedCache &c) { return c.cum[c.nseq] * c.per_seq; }
