@@ -65,9 +65,9 @@ __device__ __forceinline__ void quarter_dot(float (&v)[kPrepFirst], const float 
             const f2 vv = pack2(v[k], v[k]);
 #pragma unroll
             for (int r = 0; r < ROWS / 4; ++r) {
-                const float4 y = *(const float4 *)(x + (j0 + k) * ROWS + 4 * r);
-                acc[2 * r] = fma2(vv, pack2(y.x, y.y), acc[2 * r]);
-                acc[2 * r + 1] = fma2(vv, pack2(y.z, y.w), acc[2 * r + 1]);
+                const ulonglong2 y = *(const ulonglong2 *)(x + (j0 + k) * ROWS + 4 * r);
+                acc[2 * r] = fma2(vv, y.x, acc[2 * r]);
+                acc[2 * r + 1] = fma2(vv, y.y, acc[2 * r + 1]);
             }
         }
     }
@@ -93,10 +93,11 @@ __device__ __forceinline__ int64_t frag_row(int64_t slice, int blocks, int block
 // rows, 14 us for 2048 in blocks of 16).  The last CTA lays out the contexts instead.
 template <int kPrepRows>
 __global__ void __launch_bounds__(kPrepThreads, 3) serve_prep_kernel(PrepArgs a) {
+    constexpr int kQuads = kPrepRows / 4, kParts = kPrepThreads / 32 / kQuads;
     grid_go();
     extern __shared__ __align__(16) float qT[];  // [d][kPrepRows]
     __shared__ float red[4][kPrepRows][kPrepCols];
-    __shared__ float rmax[kPrepRows];
+    __shared__ float rmax[kParts][kPrepRows];
     __shared__ int64_t wsum[kPrepThreads / 32];
     const Prepared &P = a.P;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -164,15 +165,22 @@ __global__ void __launch_bounds__(kPrepThreads, 3) serve_prep_kernel(PrepArgs a)
             place[k] = ((at >> 4) * 32 + ((at >> 2) & 3)) * 4 + (at & 3);
         }
     }
-    for (int r = warp; r < kPrepRows; r += kPrepThreads / 32) {  // a warp a row
-        float mx = 0.f;
-        for (int j = lane; j < d; j += 32) {
-            const float x = r < nr ? load_elem(a.q, a.dtype, (r0 + r) * d + j) : 0.f;
-            qT[j * kPrepRows + r] = x;
-            mx = fmaxf(mx, fabsf(x));
+    {  // a warp four rows (stored together, for fewer bank conflicts), part of their coordinates
+        const int rq = 4 * (warp % kQuads), jp = warp / kQuads;
+        float mx[4] = {};
+        for (int j = 32 * jp + lane; j < d; j += 32 * kParts) {
+            float x[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) x[k] = rq + k < nr ? load_elem(a.q, a.dtype, (r0 + rq + k) * d + j) : 0.f;
+            *(float4 *)(qT + j * kPrepRows + rq) = make_float4(x[0], x[1], x[2], x[3]);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], fabsf(x[k]));
         }
-        mx = warp_max(mx);
-        if (lane == 0) rmax[r] = mx;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float x = warp_max(mx[k]);
+            if (lane == 0) rmax[jp][rq + k] = x;
+        }
     }
     __syncthreads();
     {
@@ -190,10 +198,13 @@ __global__ void __launch_bounds__(kPrepThreads, 3) serve_prep_kernel(PrepArgs a)
     __syncthreads();
 #pragma unroll 1
     for (int r = warp; r < nr; r += kPrepThreads / 32) {
-        const int64_t row = r0 + r, slice = row / a.rows_in;
-        const int rr = (int)(row - slice * a.rows_in), b = (int)(slice / a.Hkv), kv = (int)(slice - (int64_t)b * a.Hkv);
+        const int row = (int)r0 + r, slice = row / a.rows_in, rr = row - slice * a.rows_in;
+        const int b = slice / a.Hkv, kv = slice - b * a.Hkv;
         const int pr = b * a.rows_in + rr;
-        const float bound = rmax[r] * qbound * sqrtf((float)d);
+        float qmax = rmax[0][r];
+#pragma unroll
+        for (int k = 1; k < kParts; ++k) qmax = fmaxf(qmax, rmax[k][r]);
+        const float bound = qmax * qbound * sqrtf((float)d);
         const int e = (bound > 0.f && bound < INFINITY) ? min(max(ilogbf(bound) - 14, -126), 126) : 0;
         const float down = exp2f((float)-e);
         if (lane == 0 && cb == 0) a.fscale[row] = a.scale * kLog2eF * exp2f((float)e);
@@ -207,7 +218,7 @@ __global__ void __launch_bounds__(kPrepThreads, 3) serve_prep_kernel(PrepArgs a)
             if (oc >= n) break;
             const float x = ((red[0][r][cc] + red[1][r][cc]) + (red[2][r][cc] + red[3][r][cc])) *
                             ((oc < d ? sigma : gamma) * down);
-            if (a.qprep) a.qprep[row * n + oc] = x;
+            if (a.qprep) a.qprep[(int64_t)row * n + oc] = x;
             if (own) put_split(own + place[k], x);
             if (pre) put_split(pre + place[k], x);
             if (a.qrows)
@@ -600,14 +611,14 @@ __global__ void __launch_bounds__(kFinThreads) serve_finish_kernel(FinishArgs a)
         f2 acc[kMgRows / 2];
 #pragma unroll
         for (int r = 0; r < kMgRows / 2; ++r) acc[r] = pack2(0.f, 0.f);
-        const float4 *o4 = (const float4 *)(osm + i0 * kMgRows);
+        const ulonglong2 *o4 = (const ulonglong2 *)(osm + i0 * kMgRows);
         auto add = [&](float v, int k) {
             const f2 vv = pack2(v, v);
 #pragma unroll
             for (int r = 0; r < kMgRows / 4; ++r) {
-                const float4 x = o4[k * (kMgRows / 4) + r];
-                acc[2 * r] = fma2(vv, pack2(x.x, x.y), acc[2 * r]);
-                acc[2 * r + 1] = fma2(vv, pack2(x.z, x.w), acc[2 * r + 1]);
+                const ulonglong2 x = o4[k * (kMgRows / 4) + r];
+                acc[2 * r] = fma2(vv, x.x, acc[2 * r]);
+                acc[2 * r + 1] = fma2(vv, x.y, acc[2 * r + 1]);
             }
         };
         if (works) {
