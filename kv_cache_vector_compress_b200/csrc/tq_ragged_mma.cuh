@@ -17,7 +17,8 @@
 // weights and centroids for 16-bit outputs; F32 splits both.
 //
 // Bound by decoding: its byte permutations and logic run on the ALU pipe, which takes an instruction
-// every other cycle and is 63 to 65% busy; DRAM and the matrix instructions are far from theirs.
+// every other cycle and is 52 to 54% busy with the three or four warps a scheduler that the registers
+// allow; the matrix instructions take 13 to 16% of theirs, DRAM a quarter.
 // 256 slices of 4096 tokens on average, 4 rows, d = 128, 3 bits: 62 us, 1.7 TB/s of records and
 // weights; 32 slices of 65536, d = 256, 4 bits: 300 us, 1.8 TB/s.  More CTAs an SM with fewer
 // registers each were slower.
