@@ -18,11 +18,10 @@ namespace tq {
 
 namespace {
 
-constexpr int kSelThreads = 512;
-constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kAtOnce = 8;  // weights a thread has on their way at once
 constexpr size_t kHeldMax = 200 * 1024;  // bytes of keys that a CTA can hold
+constexpr size_t kHeldPair = 96 * 1024;  // ... that two CTAs of an SM can
 
 // (The addition makes -0 a 0 and any NaN the positive one with all other bits set.)
 __device__ __forceinline__ uint32_t weight_key(float w) {
@@ -47,9 +46,10 @@ using Step = std::integral_constant<uint32_t, N>;
 // memory find the threshold; then every warp takes a run of consecutive slots, counts what it keeps,
 // and, with the counts of the warps before it, writes the kept slots in their order.
 // Bound by instructions and the latency of the five steps: 256 slices of 4352 tokens 12 us, of 26000
-// tokens 40 us (keys in registers, 1024 threads a slice: 18 and 45 us).
-template <bool HELD>
-__global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(EvictCall c) {
+// tokens 37 us (keys in registers, 1024 threads a slice: 18 and 45 us).
+template <bool HELD, int kSelThreads>
+__global__ void __launch_bounds__(kSelThreads, 1024 / kSelThreads) evict_select_kernel(EvictCall c) {
+    constexpr int kSelWarps = kSelThreads / 32, kBinsOf = kBins / kSelThreads;  // bins of a thread
     grid_go();
     extern __shared__ uint32_t held[];  // HELD: [t_cap]
     __shared__ __align__(16) uint32_t hist[kBins];
@@ -113,7 +113,8 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(EvictCall 
     for (int pass = 0; pass < 3; ++pass) {
         const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
         const uint32_t dm = pass < 2 ? 2047u : 1023u;
-        *(uint4 *)(hist + 4 * tid) = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int k = 0; k < kBinsOf; ++k) hist[tid + k * kSelThreads] = 0;
         __syncthreads();
         if (pass == 0) {
             sweep(all_threads, false, tid, n, [&](uint32_t key, uint32_t s) {
@@ -126,10 +127,11 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(EvictCall 
             });
         }
         __syncthreads();
-        // suffix sums over the bins, four a thread, from the top: thread 0 takes the highest four
-        const uint32_t low = kBins - 4 - 4 * tid;
-        const uint4 h = *(const uint4 *)(hist + low);
-        const uint32_t mine = h.x + h.y + h.z + h.w;
+        // suffix sums over the bins from the top: thread 0 takes the highest
+        const uint32_t top = kBins - 1 - kBinsOf * tid;
+        uint32_t h[kBinsOf], mine = 0;
+#pragma unroll
+        for (int k = 0; k < kBinsOf; ++k) mine += h[k] = hist[top - k];
         uint32_t x = mine;
         for (int o = 1; o < 32; o <<= 1) {
             const uint32_t y = __shfl_up_sync(kFull, x, o);
@@ -140,14 +142,13 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(EvictCall 
         uint32_t above = x - mine;
         for (int k = 0; k < warp; ++k) above += sums[0][k];
         if (above < rank && rank <= above + mine) {
-            const uint32_t hs[4] = {h.w, h.z, h.y, h.x};
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                if (above < rank && rank <= above + hs[k]) {
-                    s_digit = low + 3 - k;
+            for (int k = 0; k < kBinsOf; ++k) {
+                if (above < rank && rank <= above + h[k]) {
+                    s_digit = top - k;
                     s_rank = rank - above;
                 }
-                above += hs[k];
+                above += h[k];
             }
         }
         __syncthreads();
@@ -261,16 +262,19 @@ __global__ void __launch_bounds__(kCopyThreads) evict_copy_kernel(EvictCall c, i
 }  // namespace
 
 cudaError_t launch_evict(const EvictCall &c, cudaStream_t s) {
-    // keys wait in shared memory wherever they fit (256 slices, read again against held: 53.3 against
-    // 51.3 us for 4352 tokens each, 147.3 against 147.0 us for 26000, the copy included)
-    const int64_t slices = c.B * (int64_t)c.Hkv;
+    // Keys wait in shared memory wherever they fit (256 slices, read again against held, the copy
+    // included: 53.3 / 51.3 us for 4352 tokens each, 147.3 / 141.9 for 26000); where only one CTA an SM
+    // does, it has the threads of two (512 threads: 147.0).
+    const unsigned slices = (unsigned)(c.B * c.Hkv);
     const size_t held = sizeof(uint32_t) * (size_t)c.t_cap;
     if (held <= kHeldMax) {
-        const cudaError_t e = allow_smem((const void *)evict_select_kernel<true>, kHeldMax);
+        const bool alone = held > kHeldPair;
+        const auto kernel = alone ? evict_select_kernel<true, 1024> : evict_select_kernel<true, 512>;
+        const cudaError_t e = allow_smem((const void *)kernel, kHeldMax);
         if (e != cudaSuccess) return e;
-        evict_select_kernel<true><<<(unsigned)slices, kSelThreads, held, s>>>(c);
+        kernel<<<slices, alone ? 1024 : 512, held, s>>>(c);
     } else {
-        evict_select_kernel<false><<<(unsigned)slices, kSelThreads, 0, s>>>(c);
+        evict_select_kernel<false, 512><<<slices, 512, 0, s>>>(c);
     }
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
