@@ -139,6 +139,27 @@ def test_shared_many_rows(tq, d, bits, B):
                seed=B + d)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("bits", [2, 3, 4])
+@pytest.mark.parametrize("dtype", ["f16", "f32"])
+def test_rows_past_eight(tq, d, bits, dtype):
+    """Blocks of eight rows, the last one not full."""
+    run_weigh(tq, dtype=dtype, d=d, bits=bits, B=3, Hq=22, Hkv=2, t_cap=170, lens=[170, 0, 45], seed=d * bits)
+
+
+@pytest.mark.parametrize("d,B,Hq", [(64, 150, 16), (128, 101, 8), (128, 110, 16), (256, 51, 16), (512, 83, 8)])
+def test_batches_of_many_rows(tq, d, B, Hq):
+    """Merges of 8 and 16 rows a CTA and preparations of 16, the last of each not full."""
+    lens = [(17 * b) % 41 for b in range(B)]
+    run_weigh(tq, dtype="bf16", d=d, B=B, Hq=Hq, Hkv=1, t_cap=40, lens=lens, seed=B)
+    run_shared(tq, dtype="bf16", d=d, B=B, Hq=Hq, Hkv=1, t_prefix=70, t_cap=40, lens=lens, seed=B)
+
+
+def test_eight_rows_over_many_stages(tq):
+    """Long enough for blocks of eight rows where there are no more than eight."""
+    run_weigh(tq, dtype="f16", d=64, bits=2, B=48, Hq=16, Hkv=2, t_cap=2400, lens=[2400] * 24 + [1000] * 24, seed=5)
+
+
 @pytest.mark.parametrize("op", ["weigh", "shared"])
 @pytest.mark.parametrize("q_scale", [0.0, 1e-4, 30.0, 3e4])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
