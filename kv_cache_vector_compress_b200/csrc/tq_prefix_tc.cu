@@ -616,8 +616,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(PrefixArgs a) {
         constexpr uint32_t is = idesc_f16_f32(128, TT), iv = idesc_f16_f32(128, D) | (1u << 16);
         const uint32_t lead = lane == 0 ? 1u : 0u;
         const uint64_t kd0 = sdesc_sw128(sbase), vd0 = sdesc_mn(sbase + C::OV, C::BLK);
+        // The scores of tile j go over the weights of tile j - SB, which that tile's value product reads
+        // from tensor memory: they wait until it is complete.  (MMAs run in the order of their issue only
+        // where they have one accumulator and shape, as the steps of one sum do; these have two.)
         auto scores = [&](int j) -> bool {
-            const int st = j & 1, sb = j % C::SB;
+            const int st = j & 1, sb = j % C::SB, old = j - C::SB;
+            if (old >= 0 && !wait_for(&bars[kVEmpty + (old & 1)], (old >> 1) & 1, abort_s)) return false;
             if (!wait_for(&bars[kKFull + st], (j >> 1) & 1, abort_s)) return false;
             tc_fence_after();
             const uint64_t kd = kd0 + (uint64_t)(st * (C::KST >> 4));
@@ -636,8 +640,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(PrefixArgs a) {
         bool ok = wait_for(&bars[kPFull + (C::SB - 1)], 0, abort_s) && scores(0);
         for (int j = 0; ok && j < nT; ++j) {
             const int st = j & 1, sb = j % C::SB;
-            // The next scores go over the weights of tile j - 1, behind their product: one thread's MMAs
-            // run in the order in which they are issued.
             if (C::SB == 2 && j + 1 < nT) ok = scores(j + 1);
             const uint32_t ph = (uint32_t)(j / C::SB + (sb == C::SB - 1 ? 1 : 0)) & 1;
             ok = ok && wait_for(&bars[kVFull + st], (j >> 1) & 1, abort_s) && wait_for(&bars[kPFull + sb], ph, abort_s);
