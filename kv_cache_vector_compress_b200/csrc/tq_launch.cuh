@@ -2,8 +2,12 @@
 //
 // A kernel launched by launch_after may start while the one before it in the stream still runs (its
 // CTAs come in as those of the other have all started and leave room).  It waits with grid_wait
-// before it touches anything that the other writes, or writes anything that it reads; every kernel
-// that such a launch follows says grid_go when that may happen.
+// before it touches anything that a kernel of the call writes, or writes anything that one reads;
+// every kernel that such a launch follows says grid_go when that may happen.  The wait is for the
+// kernel before, and for the others through it, since each of them has waited as well; that a kernel
+// has been let start says nothing of what it may read.  Before its wait a kernel reads only what was
+// there before the call (the parameter set, records): a call's first launch is an ordinary one,
+// behind all earlier work.
 #pragma once
 
 #include <cuda_runtime.h>

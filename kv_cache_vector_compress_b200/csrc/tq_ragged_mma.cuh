@@ -146,17 +146,12 @@ __global__ void __launch_bounds__(NW * 32, D >= 256 || F32 || NT > 1 ? 3 : 4)
     // 2-bit keys: the four centroids as pairs of bytes; 2^16 where the compiler does not see it
     const uint32_t kp0 = T->kh[0] | ((uint32_t)T->kh[1] << 16), kp1 = T->kh[2] | ((uint32_t)T->kh[3] << 16);
     const uint32_t k16 = pair.two16;
-    // Behind the many-row prefix kernel this one runs beside it: that kernel lets it start when its own
-    // wait for the preparation is over, and the wait at the end makes the merge wait for both.
-    if (!pair.late_wait) grid_wait();
+    grid_wait();
     grid_go();
     const int64_t total = ragged_total(a.c);
     const int64_t w1 = cta_first(total, a.c.ctas, cta + 1);
     int64_t w = cta_first(total, a.c.ctas, cta);
-    if (w >= w1) {
-        grid_wait();
-        return;
-    }
+    if (w >= w1) return;
     const int r0 = rblk * C::ROWS, nr = min(C::ROWS, a.c.rows - r0);
     uint8_t *ring = smem + (size_t)warp * C::NST * C::STAGE;
     float4 *meta = (float4 *)(smem + C::OMETA) + warp * 32;
@@ -536,7 +531,6 @@ __global__ void __launch_bounds__(NW * 32, D >= 256 || F32 || NT > 1 ? 3 : 4)
             }
         }
     }
-    grid_wait();
 }
 
 template <int D, int KB, int NT, bool F32>

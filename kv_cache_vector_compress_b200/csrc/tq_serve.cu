@@ -452,13 +452,10 @@ __device__ __forceinline__ void weigh_tokens(const FinishArgs &a, unsigned id, f
     constexpr int PT = kWtTokens / THREADS;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, ps = partial_stride(a.P.d);
     const int slice = (int)(id / a.chunks), R = a.own.rows;
-    const int len = a.own.len[slice / a.own.per_seq];
     const int t0 = (int)(id - (unsigned)slice * a.chunks) * kWtTokens + tid;
-    if (t0 - tid >= len) {
-        grid_wait();
-        return;
-    }
     grid_wait();
+    const int len = a.own.len[slice / a.own.per_seq];
+    if (t0 - tid >= len) return;
     float s[PT] = {};
     for (int r0 = 0; r0 < R; r0 += kWtRows) {
         const int nr = min(kWtRows, R - r0);
@@ -516,12 +513,11 @@ __global__ void __launch_bounds__(kFinThreads) serve_finish_kernel(FinishArgs a)
 #pragma unroll
     for (int k = 0; k < 32; ++k) first[k] = works && k < part ? w[(int64_t)k * d] : 0.f;
     {
-        // where the row's partials are: the preparation, whose lengths this takes, is over (the kernel
-        // before lets this one start behind its own wait for it)
         const int r4 = warp / kMgWarps, q = warp % kMgWarps;
         const int64_t row = row0 + r4;
         Parts g[2] = {{nullptr, 0, 0}, {nullptr, 0, 0}};
-        if (row < a.rows) {
+        grid_wait();
+        if (row < a.rows) {  // where the row's partials are
             const int slice = (int)(row / a.rows_in), r = (int)(row - (int64_t)slice * a.rows_in);
             const int b = slice / a.Hkv, kv = slice - b * a.Hkv;
             if (a.tc_splits) {
@@ -533,7 +529,6 @@ __global__ void __launch_bounds__(kFinThreads) serve_finish_kernel(FinishArgs a)
             }
             g[1] = parts_of(a.own, a.own_part, slice, r, ps);
         }
-        grid_wait();
         // the prefix's partials, then the own ones, as one list; this warp's share of it
         const int all = g[0].n + g[1].n, per = (all + kMgWarps - 1) / kMgWarps;
         const int p0 = min(q * per, all), p1 = min(p0 + per, all);
@@ -716,7 +711,6 @@ cudaError_t launch_ragged_mma(const RaggedArgs &own, const RaggedArgs &prefix, c
     p.a[0] = own;
     p.a[1] = prefix;
     p.two16 = 1u << 16;
-    p.late_wait = plan.tc.splits > 0;
     auto blocks = [&](const RaggedCache &c) { return (c.rows + plan.row_block - 1) / plan.row_block; };
     p.first = plan.own_ctas ? plan.own_ctas * blocks(own.c) : 0;
     p.total = p.first + (plan.prefix_ctas ? plan.prefix_ctas * blocks(prefix.c) : 0);

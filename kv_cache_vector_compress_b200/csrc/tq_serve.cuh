@@ -227,7 +227,6 @@ int ragged_mma_ctas_per_sm(const Prepared &P);
 struct RaggedPair {
     RaggedArgs a[2];
     uint32_t two16;    // 65536
-    int late_wait;     // behind the many-row prefix kernel, which it needs nothing of
     int first, total;  // CTAs of a[0], and of both; CTA i of a cache: division i % ctas, row block i / ctas
 };
 cudaError_t launch_ragged_mma(const RaggedArgs &own, const RaggedArgs &prefix, const ServePlan &plan, bool f32,
