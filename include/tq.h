@@ -389,7 +389,8 @@ tq_status tq_attend_shared(const tq_params *p, const void *q, tq_dtype dtype, in
  *   out                  as tq_attend_shared without a prefix
  *   weights[b, h, t] +=  sum over the Hq/Hkv * Nq query rows of KV head h of softmax_t(scale * s_t),
  *                        for t < lens[b]; entries behind are left as they are
- *   weights : device fp32 [B, Hkv, t_cap]
+ *   weights : device fp32 [B, Hkv, t_cap].  The call adds to what is there: the caller clears a
+ *             token's weight when the token enters the cache
  * The other arguments are those of tq_attend_shared; t_cap >= 1.  In the scores the query rows keep
  * 22 bits whatever dtype is, and the key centroids 20 or more; with the 16-bit types, centroids of
  * 4-bit parameter sets are off by 3.1e-5 of themselves at most.  The rows are added in ascending
@@ -414,7 +415,9 @@ tq_status tq_attend_weigh(const tq_params *p, const void *q, tq_dtype dtype, int
  *   weights     : device fp32 [B, Hkv, t_cap].  A NaN counts as heavier than any number
  *   budget      : 1 .. t_cap;  recent: 0 .. budget
  *   out_cap     : capacity of the destination, >= budget: [B, Hkv, out_cap] records and weights.
- *                 Slots behind the kept tokens are left as they are.  The destination must not
+ *                 Slots behind the kept tokens are left as they are, their weights too: where the
+ *                 destination was used before, those are of tokens that are gone, and the caller
+ *                 clears them before tq_attend_weigh adds to them.  The destination must not
  *                 overlap the source (TQ_ERR_INVALID_ARG)
  *   kept        : device int32 [B, Hkv, budget], the kept slots in ascending order; entries behind
  *                 the last one are left as they are

@@ -501,8 +501,8 @@ def tq_attend_weigh(p: Params, q: torch.Tensor, keys, values, lens: torch.Tensor
                     weights: torch.Tensor, scale: float = 0.0, out=None, scratch=None, dev_status=None):
     """Attention of q [B, Hq, Nq, dim] (float16, bfloat16 or float32) over the first lens[b] tokens of
     each sequence's cache (records [B, Hkv, t_cap]).  Adds to weights (float32 [B, Hkv, t_cap], in
-    place) the softmax weight every token got, summed over the query rows of its KV head.  Returns
-    the output, of q's type."""
+    place; zero for a token that is new) the softmax weight every token got, summed over the query
+    rows of its KV head.  Returns the output, of q's type."""
     B, Hq, Nq, d = q.shape
     dt, dev = _row_dtype(q.dtype), _device(p, q)
     n = B * Hq * Nq * p.dim
@@ -530,7 +530,9 @@ def tq_evict(p: Params, keys, values, weights: torch.Tensor, lens: torch.Tensor,
     `recent` ones always among them, in their order into a cache of capacity out_cap.  Returns
     (out_keys, out_values, out_weights, kept, out_lens): the destination cache, its weights
     [B, Hkv, out_cap], the kept slots int32 [B, Hkv, budget] and the new lengths int32 [B].
-    Entries behind a slice's kept tokens are not written."""
+    Entries behind a slice's kept tokens are not written.  tq_attend_weigh adds to the weights, so
+    those of tokens still to come have to be zero: they are in an out_weights made here; in one that
+    is passed in, the caller clears out_weights[b, :, out_lens[b]:]."""
     B, dev = lens.numel(), _device(p, lens)
     n, m = B * Hkv * t_cap, B * Hkv * out_cap
     new = lambda *shape, dtype: torch.empty(shape, dtype=dtype, device=lens.device)  # noqa: E731
@@ -540,7 +542,7 @@ def tq_evict(p: Params, keys, values, weights: torch.Tensor, lens: torch.Tensor,
     if out_values is None:
         out_values = (new(m, p.value_words(), dtype=torch.int32), new(m, dtype=torch.float16))
     if out_weights is None:
-        out_weights = new(B, Hkv, out_cap, dtype=torch.float32)
+        out_weights = torch.zeros(B, Hkv, out_cap, device=lens.device)
     if kept is None:
         kept = new(B, Hkv, budget, dtype=torch.int32)
     if out_lens is None:
