@@ -1,6 +1,7 @@
 // tq_serve.cu -- what surrounds the attention kernels of tq_attend_shared and tq_attend_weigh: the
 // preparation of the query rows and operand tables, the merge of the partial results and the
 // addition of the softmax weights; and the plain kernel for the shapes without a tensor-core one.
+#include <float.h>
 #include <math.h>
 
 #include <atomic>
@@ -271,7 +272,8 @@ __global__ void __launch_bounds__(kPlThreads) ragged_plain_kernel(RaggedArgs a) 
 #pragma unroll
             for (int c = 0; c < kPlCoord; ++c) o[r][c] = 0.f;
         }
-        if (tid < kPlRows) rowN[tid] = -INFINITY;
+        // (a finite first reference: NaN, which a maximum leaves out, and -infinity make their own weights)
+        if (tid < kPlRows) rowN[tid] = -FLT_MAX;
         __syncthreads();
         for (int t0 = (int)(pc.s0 * kStage); t0 < t_end; t0 += kPlTile) {
             const int t = t0 + tid, nt = min(kPlTile, t_end - t0);
@@ -306,7 +308,8 @@ __global__ void __launch_bounds__(kPlThreads) ragged_plain_kernel(RaggedArgs a) 
                     }
                 }
                 const float kn = f16_bits_to_f32(a.c.knorm[rec]), rho = f16_bits_to_f32(a.c.krnorm[rec]);
-                const float vn = fmaxf(f16_bits_to_f32(a.c.vnorm[rec]), kMinNorm), lv = log2f(vn);
+                const float vr = f16_bits_to_f32(a.c.vnorm[rec]), vn = fmaxf(vr, kMinNorm);
+                const float lv = vr != vr ? vr : log2f(vn);
                 rv = 1.f / vn;
 #pragma unroll
                 for (int r = 0; r < kPlRows; ++r) {
@@ -327,12 +330,12 @@ __global__ void __launch_bounds__(kPlThreads) ragged_plain_kernel(RaggedArgs a) 
                 float mx = old;
                 for (int u = 0; u < kPlThreads / 32; ++u) mx = fmaxf(mx, red[tid][u]);
                 rowN[tid] = mx;
-                rowA[tid] = old == -INFINITY ? 0.f : exp2f(old - mx);
+                rowA[tid] = exp2f(old - mx);
             }
             __syncthreads();
 #pragma unroll
             for (int r = 0; r < kPlRows; ++r) {
-                const float N = rowN[r], w8 = N == -INFINITY ? 0.f : exp2f(y[r] - N);
+                const float w8 = exp2f(y[r] - rowN[r]);
                 ps[r * kPlTile + tid] = w8;
                 l[r] = fmaf(l[r], rowA[r], w8 * rv);
 #pragma unroll

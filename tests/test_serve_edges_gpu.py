@@ -31,3 +31,40 @@ def test_weights_of_tokens_to_come_are_zero(tq):  # noqa: F811
     before = w.sum(-1)
     tq.tq_attend_weigh(pr.p, pr.q, k, v, pr.dlens, Hkv, cap, w)
     torch.testing.assert_close(w.sum(-1) - before, torch.full((B, Hkv), 2.0, device="cuda"), rtol=0, atol=1e-4)
+
+
+@pytest.mark.parametrize("d,m,bits", [(32, 32, 2), (128, 64, 3), (128, 32, 3), (512, 256, 4), (256, 128, 2)])
+@pytest.mark.parametrize("where", ["query", "key norms", "key norm", "value norm"])
+def test_nan_is_not_lost(tq, d, m, bits, where):  # noqa: F811
+    """A NaN reaches every row that it concerns, whatever kernel the shape has, and no other row: in a query;
+    in the norms of a slice's last 200 records; in the one record of a short slice; in one value norm."""
+    import torch
+    B, Hq, Hkv, cap = 3, 4, 2, 1500
+    pr = Problem(tq, dtype="f32", d=d, m=m, bits=bits, B=B, Hq=Hq, Hkv=Hkv, t_cap=cap, lens=[1500, 900, 1], seed=62)
+    want, wantw = pr.shared(tq), torch.from_numpy(pr.w0).cuda()
+    pr.weigh(tq, wantw)
+    bad = np.zeros((B, Hq), bool)
+    slot = lambda b, h, t: (b * Hkv + h) * cap + t  # noqa: E731
+    if where == "query":
+        pr.q[1, 3] = float("nan")
+        bad[1, 3] = True
+    elif where == "key norms":
+        pr.own.kn[slot(0, 1, 1300):slot(0, 1, 1500)] = np.nan
+        bad[0, 2:] = True
+    elif where == "key norm":
+        pr.own.kn[slot(2, 0, 0)] = np.nan
+        bad[2, :2] = True
+    else:
+        pr.own.vn[slot(1, 0, 333)] = np.nan
+        bad[1, :2] = True
+    pr.k, pr.v = pr.own.device()
+    w = torch.from_numpy(pr.w0).cuda()
+    bad = torch.from_numpy(bad).cuda()
+    for out in (pr.shared(tq), pr.weigh(tq, w)):
+        nan = torch.isnan(out).flatten(2)
+        assert nan[bad].all() and not nan[~bad].any()
+        torch.testing.assert_close(out[~bad], want[~bad], rtol=1e-4, atol=1e-5)
+    heads = bad.view(B, Hkv, -1).any(-1)
+    there = torch.arange(cap, device="cuda") < pr.dlens[:, None, None]
+    assert torch.isnan(w)[heads[..., None] & there].all()
+    torch.testing.assert_close(w[~heads], wantw[~heads], rtol=1e-4, atol=1e-5)
