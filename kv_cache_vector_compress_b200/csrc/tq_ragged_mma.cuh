@@ -217,7 +217,9 @@ __global__ void __launch_bounds__(NW * 32, D >= 256 || F32 || NT > 1 ? 3 : 4)
         for (int t = 0; t < NT; ++t) {
             const int row = 4 * t + t4;
             f[t] = row < nr ? a.fscale[ragged_row(a.c, pc.slice, r0 + row)] : 0.f;
-            N[t] = -FLT_MAX;
+            // Rows that fill the block hold whatever the scratch held.  They stay in their own columns, and
+            // with this reference they never call for a rescaling, which moves all rows' references.
+            N[t] = row < nr ? -FLT_MAX : INFINITY;
             l[t] = 0.f;
         }
 #pragma unroll
