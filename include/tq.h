@@ -369,7 +369,9 @@ tq_status tq_attend_static(const tq_params *p, const float *q, int B, int Hq, in
  *   scratch  : tq_attend_shared_scratch_bytes(...) bytes; calls that share it must not overlap
  * Precision: sums, maxima and normalisers are in 32 bits.  With TQ_F32 every operand of a product
  * keeps 20 bits or more (fp16 pairs hi + lo; fp32 where there is no tensor-core kernel).  With the
- * 16-bit types operands are rounded to fp16 (relative 2^-11).
+ * 16-bit types operands are rounded to fp16 (relative 2^-11).  A softmax weight (times its value's
+ * norm, but for many rows on a prefix) keeps that precision down to 2^-21 of the largest one of the
+ * row that a CTA sums it with, and is off by 2^-32 of that at most below (TQ_F32: 20 bits down to 2^-12).
  * TQ_ERR_UNSUPPORTED when t_prefix or t_cap exceeds 2^31 - 1024 or B * Hq * Nq exceeds 262140.
  */
 size_t tq_attend_shared_scratch_bytes(const tq_params *p, tq_dtype dtype, int B, int Hq, int Hkv, int Nq,

@@ -8,12 +8,12 @@
 // so that a weight is one fused multiply-add and one exponential of its score.  Both are scaled by
 // powers of two, 2^k and 2^s, one of each a tile, that put the tile's largest norm in [2^10, 2^11):
 // the products stay inside fp16 whatever the norms are.  With z = f 2^-k S and a reference
-// N >= z - s - 8, W = 2^(z - s - N), and the normaliser is 2^s sum W: the partial result
+// N >= z - s - 15, W = 2^(z - s - N), and the normaliser is 2^s sum W: the partial result
 // (N, l, o) is that of tq_serve.cuh.
 //
 // Roles: eight softmax warps (two threads a row, half of a tile's tokens each), eight decoder warps,
 // one warp that issues the MMAs.  The softmax first takes the weights with the reference as it is;
-// if any comes out above 2^8 (the first tile, hardly ever later) the tile is done again with a new
+// if any comes out above 2^15 (the first tile, hardly ever later) the tile is done again with a new
 // reference, so that the usual path needs no maximum before its exponentials.
 // Q stays in tensor memory as the A operand and W is written over the scores it came from, so that
 // shared memory carries only the decoded tiles: with both operands in shared memory a 128 x 128 x 16
@@ -364,7 +364,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(PrefixArgs a) {
                 return top;
             };
             const __half2 top = weigh();
-            const bool over = fmaxf(__low2float(top), __high2float(top)) > 256.f;
+            static_assert(kHeadroom == 15.f, "2^15");
+            const bool over = fmaxf(__low2float(top), __high2float(top)) > 32768.f;
             const bool any = __any_sync(kFull, over);
             if (lane == 0) flags[(j & 1) * 8 + 4 * h + quarter] = any || !ok;
             tc_fence_before();
@@ -384,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(PrefixArgs a) {
                 xch[128 * h + r128] = mx;
                 pair_sync();
                 mx = fmaxf(mx, xch[128 * (1 - h) + r128]);
-                const float up = mx > N + 8.f ? mx : N, sc = exp2f(N - up);
+                const float up = mx > N + kHeadroom ? mx - kTopWeight : N, sc = exp2f(N - up);
                 N = up;
                 l2 = mul2(l2, pack2(sc, sc));
                 if (j > 0) {

@@ -123,7 +123,7 @@ __device__ __forceinline__ float lg2(float x) {
 // takes every NW-th stage of a piece through its own ring of asynchronous copies and keeps its own
 // reference, sums and accumulators; they meet at the end of the piece.
 //
-// The reference N of a row moves only when some y exceeds it by more than 8: then the accumulators
+// The reference N of a row moves only when some y exceeds it by more than 15: then the accumulators
 // are rescaled (rare after the first stages), so that the usual path has no reduction over lanes.
 template <int D, int KB, int NT, bool F32>
 __global__ void __launch_bounds__(NW * 32, D >= 256 || F32 || NT > 1 ? 3 : 4)
@@ -364,7 +364,7 @@ __global__ void __launch_bounds__(NW * 32, D >= 256 || F32 || NT > 1 ? 3 : 4)
                     }
                     yA[t] = zA + mA.z;
                     yB[t] = zB + mB.z;
-                    over |= fmaxf(yA[t], yB[t]) > N[t] + 8.f;
+                    over |= fmaxf(yA[t], yB[t]) > N[t] + kHeadroom;
                 }
                 if (__any_sync(kFull, over)) {
 #pragma unroll
@@ -373,7 +373,7 @@ __global__ void __launch_bounds__(NW * 32, D >= 256 || F32 || NT > 1 ? 3 : 4)
                         mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 4));
                         mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 8));
                         mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 16));
-                        mx = fmaxf(mx, N[t]);
+                        mx = fmaxf(mx - kTopWeight, N[t]);
                         const float sc = exp2f(N[t] - mx);
                         N[t] = mx;
                         l[t] *= sc;

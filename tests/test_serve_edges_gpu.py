@@ -101,3 +101,47 @@ def test_results_do_not_depend_on_the_scratch(tq, dtype, d, bits, G):  # noqa: F
     for other in got[1:]:
         for a, b in zip(got[0], other):
             assert torch.equal(a, b)
+
+
+def two_kinds(tq, dtype, d, bits, B, Hq, t_prefix, t_cap, z_top, z_low, seed):  # noqa: F811
+    """A Problem whose records are of two kinds, the query the same in every row: logits z_top and z_low (to
+    the rounding of the query).  Returns it, the two records and the exact (logits [2], values [2, d])."""
+    import math
+    import torch
+    pr = Problem(tq, dtype=dtype, d=d, bits=bits, B=B, Hq=Hq, Hkv=1, t_prefix=0, t_cap=1, seed=seed)
+    two = ref.Cache(2, d, pr.m, bits, seed, zero=0.0)
+    two.kc[1] = two.kc[0]
+    two.kn[:] = 8.0, 8.0 * z_low / z_top
+    two.kr[:] = 0
+    two.vn[:] = 8.0
+    kc, _, v = two.dequantized()
+    R = pr.R.astype(np.float64)
+    q = R.T @ kc[0] * (z_top * math.sqrt(d) / (8.0 * (kc[0] ** 2).sum()))
+    pr.q = torch.from_numpy(q).to(pr.q.dtype).expand(B, Hq, 1, d).contiguous().cuda()
+    q = pr.q[0, 0, 0].double().cpu().numpy()
+    pr.t_prefix, pr.t_cap = t_prefix, t_cap
+    z = two.kn.astype(np.float64) * ((R @ q) @ kc[0]) / math.sqrt(d)
+    return pr, two.device(), z, v @ R
+
+
+def test_light_tokens_of_a_long_prefix_count(tq):  # noqa: F811
+    """Four million tokens, 2^-25.3 of the two heaviest ones' weight each, make up 5% of the softmax: too
+    light for fp16 beside a weight of 1.  A weight is held to half a step of fp16 at 2^7 times that, 2^-32 of
+    the largest, so that half the prefix (one of its two splits) is off by 2^21 2^-32."""
+    import torch
+    d, T, rows = 64, 1 << 22, 128 * 74
+    pr, (k2, v2), z, v = two_kinds(tq, "f16", d, 2, rows // 64, 64, T, 0, 35.0, 17.5, 64)
+    kind = torch.ones(T, dtype=torch.long, device="cuda")
+    kind[0] = kind[T // 2] = 0
+    pr.pk, pr.pv = tuple(t[kind].contiguous() for t in k2), tuple(t[kind].contiguous() for t in v2)
+    out = pr.shared(tq).double().cpu().numpy().reshape(rows, d)
+    light = (T - 2) * np.exp(z[1] - z[0])
+    assert 0.05 < light < 0.2
+    want = (2 * v[0] + light * v[1]) / (2 + light)
+    # logits of operands rounded to fp16 (query and key) are off by 2 2^-11 of themselves and move the light
+    # share by as much as their difference; the sums' operands (weight and value) by 2 2^-11, the output by 2^-11.
+    # The 32-bit sum takes 16 tokens at a time, 2^17 times, and each time may lose 2^-23 of what it holds
+    tol = (light / (2 + light) * 2 * 2.0 ** -11 * (abs(z[0]) + abs(z[1])) + 2.0 ** 21 * 2.0 ** -32 + 3 * 2.0 ** -11
+           + 2.0 ** 17 * 2.0 ** -23)
+    err = np.linalg.norm(out - want, axis=1)
+    assert err.max() <= tol * np.linalg.norm(v, axis=1).max(), (err.max(), tol)
