@@ -419,12 +419,14 @@ tq_status tq_attend_weigh(const tq_params *p, const void *q, tq_dtype dtype, int
  *   out_cap     : capacity of the destination, >= budget: [B, Hkv, out_cap] records and weights.
  *                 Slots behind the kept tokens are left as they are, their weights too: where the
  *                 destination was used before, those are of tokens that are gone, and the caller
- *                 clears them before tq_attend_weigh adds to them.  The destination must not
- *                 overlap the source (TQ_ERR_INVALID_ARG)
+ *                 clears them before tq_attend_weigh adds to them
  *   kept        : device int32 [B, Hkv, budget], the kept slots in ascending order; entries behind
  *                 the last one are left as they are
- *   out_lens    : device int32 [B], min(n, budget); must not be lens
+ *   out_lens    : device int32 [B], min(n, budget)
  *   scratch     : tq_evict_scratch_bytes(...) bytes
+ * What the call writes (the destination's arrays, out_weights, kept, out_lens, scratch, dev_status)
+ * may overlap neither what it reads (the source's arrays, weights, lens) nor one another
+ * (TQ_ERR_INVALID_ARG).
  */
 size_t tq_evict_scratch_bytes(const tq_params *p, int B, int Hkv, int64_t t_cap, int64_t budget);
 tq_status tq_evict(const tq_params *p, int B, int Hkv, const int32_t *lens, int64_t t_cap, const uint32_t *kcodes,

@@ -98,9 +98,24 @@ RaggedCache cache_of(const uint32_t *kcodes, const uint32_t *ksigns, const uint1
     return c;
 }
 
-bool overlap(const void *a, size_t na, const void *b, size_t nb) {
-    const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
-    return x < y + nb && y < x + na;
+// What a call reads and what it writes.
+struct Range {
+    const void *at;
+    size_t bytes;
+};
+bool overlap(const Range &a, const Range &b) {
+    const uintptr_t x = (uintptr_t)a.at, y = (uintptr_t)b.at;
+    return a.at && b.at && x < y + b.bytes && y < x + a.bytes;
+}
+// No written range may lie in one that is read, nor in another written one.
+bool apart(const Range *written, int nw, const Range *read, int nr) {
+    for (int i = 0; i < nw; ++i) {
+        for (int j = 0; j < nr; ++j)
+            if (overlap(written[i], read[j])) return false;
+        for (int j = 0; j < i; ++j)
+            if (overlap(written[i], written[j])) return false;
+    }
+    return true;
 }
 
 }  // namespace
@@ -182,17 +197,18 @@ tq_status tq_evict(const tq_params *p, int B, int Hkv, const int32_t *lens, int6
         c.dst[i] = dst[i];
         c.bytes[i] = bytes[i];
     }
-    // nothing that the call writes may lie in what it reads: the copies run in no order
+    // The copies run in no order and take the kept slots and counts from memory.
+    Range read[kEvictArrays + 1], written[kEvictArrays + 4];
     for (int i = 0; i < kEvictArrays; ++i) {
-        const size_t nd = (size_t)n_dst * bytes[i];
-        for (int j = 0; j < kEvictArrays; ++j)
-            if (overlap(dst[i], nd, src[j], (size_t)n_src * bytes[j])) return TQ_ERR_INVALID_ARG;
-        if (overlap(dst[i], nd, lens, sizeof(int32_t) * (size_t)B)) return TQ_ERR_INVALID_ARG;
+        read[i] = {src[i], (size_t)n_src * bytes[i]};
+        written[i] = {dst[i], (size_t)n_dst * bytes[i]};
     }
-    for (int j = 0; j < kEvictArrays; ++j)
-        if (overlap(kept, sizeof(int32_t) * (size_t)(B * (int64_t)Hkv * budget), src[j], (size_t)n_src * bytes[j]))
-            return TQ_ERR_INVALID_ARG;
-    if (overlap(out_lens, sizeof(int32_t) * (size_t)B, lens, sizeof(int32_t) * (size_t)B)) return TQ_ERR_INVALID_ARG;
+    read[kEvictArrays] = {lens, sizeof(int32_t) * (size_t)B};
+    written[kEvictArrays] = {kept, sizeof(int32_t) * (size_t)(B * (int64_t)Hkv * budget)};
+    written[kEvictArrays + 1] = {out_lens, sizeof(int32_t) * (size_t)B};
+    written[kEvictArrays + 2] = {scratch, evict_scratch_bytes(B, Hkv)};
+    written[kEvictArrays + 3] = {dev_status, sizeof(int32_t)};
+    if (!apart(written, kEvictArrays + 4, read, kEvictArrays + 1)) return TQ_ERR_INVALID_ARG;
     c.B = B;
     c.Hkv = Hkv;
     c.lens = lens;
