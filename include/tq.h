@@ -367,6 +367,8 @@ tq_status tq_attend_static(const tq_params *p, const float *q, int B, int Hq, in
  *   scale    : as tq_attend
  *   out      : device [B, Hq, Nq, dim] of dtype
  *   scratch  : tq_attend_shared_scratch_bytes(...) bytes; calls that share it must not overlap
+ * What the call writes (out, scratch, dev_status) may overlap neither what it reads nor one another
+ * (TQ_ERR_INVALID_ARG); out may be q.
  * Precision: sums, maxima and normalisers are in 32 bits.  With TQ_F32 every operand of a product
  * keeps 20 bits or more (fp16 pairs hi + lo; fp32 where there is no tensor-core kernel).  With the
  * 16-bit types operands are rounded to fp16 (relative 2^-11).  A softmax weight (times its value's
@@ -398,6 +400,7 @@ tq_status tq_attend_shared(const tq_params *p, const void *q, tq_dtype dtype, in
  * 4-bit parameter sets are off by 3.1e-5 of themselves at most.  The rows are added in ascending
  * order: results are bit-identical run to run.
  *   scratch : tq_attend_weigh_scratch_bytes(...) bytes, among them 4 for each (query row, slot)
+ * weights counts as written (see tq_attend_shared).
  */
 size_t tq_attend_weigh_scratch_bytes(const tq_params *p, tq_dtype dtype, int B, int Hq, int Hkv, int Nq,
                                      int64_t t_cap);

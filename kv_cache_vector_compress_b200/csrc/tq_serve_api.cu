@@ -39,6 +39,26 @@ tq_status check_shape(tq_dtype dtype, int B, int Hq, int Hkv, int Nq, int64_t t_
 
 bool good(const void *p) { return p && aligned16(p); }
 
+// What a call reads and what it writes.
+struct Range {
+    const void *at;
+    size_t bytes;
+};
+bool overlap(const Range &a, const Range &b) {
+    const uintptr_t x = (uintptr_t)a.at, y = (uintptr_t)b.at;
+    return a.at && b.at && x < y + b.bytes && y < x + a.bytes;
+}
+// No written range may lie in one that is read, nor in another written one.
+bool apart(const Range *written, int nw, const Range *read, int nr) {
+    for (int i = 0; i < nw; ++i) {
+        for (int j = 0; j < nr; ++j)
+            if (overlap(written[i], read[j])) return false;
+        for (int j = 0; j < i; ++j)
+            if (overlap(written[i], written[j])) return false;
+    }
+    return true;
+}
+
 // One attention call; weights is null for tq_attend_shared.
 tq_status attend(const tq_params *p, const void *q, tq_dtype dtype, int B, int Hq, int Hkv, int Nq, int64_t t_prefix,
                  const RaggedCache &prefix, const int32_t *lens, int64_t t_cap, const RaggedCache &own, float scale,
@@ -62,6 +82,26 @@ tq_status attend(const tq_params *p, const void *q, tq_dtype dtype, int B, int H
     call.P = prepared_view(p);
     const ServePlan plan = plan_serve(call.P, dtype, B, Hq, Hkv, Nq, t_prefix, t_cap, weights != nullptr);
     if (scratch_bytes < plan.total) return TQ_ERR_INVALID_ARG;
+    // Kernels of the call run beside one another, and one reads what another has left in the scratch.
+    // (out may be q: it is written when the rows have been read.)
+    const size_t rows = (size_t)B * Hq * Nq * p->dim * (dtype == TQ_F32 ? 4 : 2), d = p->dim;
+    Range read[15] = {{q, rows}, {p->workspace, ws_layout(p->dim, p->proj_dim).total}, {t_cap > 0 ? lens : nullptr, sizeof(int32_t) * (size_t)B}};
+    const Range written[4] = {{scratch, plan.total},
+                              {weights, sizeof(float) * (size_t)B * Hkv * (size_t)t_cap},
+                              {dev_status, sizeof(int32_t)},
+                              {out, rows}};
+    int nr = 3;
+    for (const RaggedCache *c : {&prefix, &own}) {
+        const size_t n = c == &prefix ? (size_t)Hkv * t_prefix : (size_t)B * Hkv * t_cap;
+        if (n == 0) continue;
+        read[nr++] = {c->kcodes, n * ((p->bits - 1) * d / 8)};
+        read[nr++] = {c->ksigns, n * (size_t)(p->proj_dim / 8)};
+        read[nr++] = {c->knorm, n * 2};
+        read[nr++] = {c->krnorm, n * 2};
+        read[nr++] = {c->vcodes, n * (p->bits * d / 8)};
+        read[nr++] = {c->vnorm, n * 2};
+    }
+    if (!apart(written, 3, read, 1) || !apart(written, 4, read + 1, nr - 1)) return TQ_ERR_INVALID_ARG;
     call.q = q;
     call.out = out;
     call.dtype = dtype;
@@ -96,26 +136,6 @@ RaggedCache cache_of(const uint32_t *kcodes, const uint32_t *ksigns, const uint1
     c.vcodes = vcodes;
     c.vnorm = vnorm;
     return c;
-}
-
-// What a call reads and what it writes.
-struct Range {
-    const void *at;
-    size_t bytes;
-};
-bool overlap(const Range &a, const Range &b) {
-    const uintptr_t x = (uintptr_t)a.at, y = (uintptr_t)b.at;
-    return a.at && b.at && x < y + b.bytes && y < x + a.bytes;
-}
-// No written range may lie in one that is read, nor in another written one.
-bool apart(const Range *written, int nw, const Range *read, int nr) {
-    for (int i = 0; i < nw; ++i) {
-        for (int j = 0; j < nr; ++j)
-            if (overlap(written[i], read[j])) return false;
-        for (int j = 0; j < i; ++j)
-            if (overlap(written[i], written[j])) return false;
-    }
-    return true;
 }
 
 }  // namespace

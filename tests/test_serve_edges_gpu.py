@@ -145,3 +145,17 @@ def test_light_tokens_of_a_long_prefix_count(tq):  # noqa: F811
            + 2.0 ** 17 * 2.0 ** -23)
     err = np.linalg.norm(out - want, axis=1)
     assert err.max() <= tol * np.linalg.norm(v, axis=1).max(), (err.max(), tol)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "f32"])
+@pytest.mark.parametrize("d,m", [(128, 64), (128, 32)])
+def test_out_may_be_the_queries(tq, dtype, d, m):  # noqa: F811
+    import torch
+    pr = Problem(tq, dtype=dtype, d=d, m=m, B=9, Hq=8, Hkv=2, t_prefix=300, t_cap=200, seed=66)
+    a, w1, w2 = pr.shared(tq), torch.from_numpy(pr.w0).cuda(), torch.from_numpy(pr.w0).cuda()
+    b = pr.weigh(tq, w1)
+    q = pr.q
+    pr.q = q.clone()
+    assert torch.equal(a, pr.shared(tq, out=pr.q))
+    pr.q = q.clone()
+    assert torch.equal(b, pr.weigh(tq, w2, out=pr.q)) and torch.equal(w1, w2)

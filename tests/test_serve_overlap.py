@@ -40,3 +40,40 @@ def test_evict_refuses_what_it_writes_in_other_memory(lib, name):  # noqa: F811
             at = blocks(SIZES)
             at[i] = at[j] + off  # from its first bytes, in its last ones, or up to its first ones
             assert evict(lib, at) == 1, (name, other, off)
+
+
+ROWS = B * 4 * 128 * 2  # f16 queries of four heads
+A_NAMES = (["workspace", "lens"] + [f"prefix {i}" for i in range(6)] + [f"own {i}" for i in range(6)] +
+           ["q", "out", "scratch", "dev_status", "weights"])
+
+
+def attend(L, sizes, at, weigh):
+    ws, lens, pre, own, (q, out, scratch, status, weights) = at[0], at[1], at[2:8], at[8:14], at[14:]
+    prm = params(L)
+    prm.workspace = ws
+    if weigh:
+        return L.tq_attend_weigh(ctypes.byref(prm), q, 0, B, 4, HKV, 1, lens, CAP, *own, 0.0, weights, out, scratch,
+                                 sizes[16], status, None)
+    return L.tq_attend_shared(ctypes.byref(prm), q, 0, B, 4, HKV, 1, 70, *pre, lens, CAP, *own, 0.0, out, scratch,
+                              sizes[16], status, None)
+
+
+@pytest.mark.parametrize("weigh", [False, True])
+@pytest.mark.parametrize("name", ["out", "scratch", "dev_status", "weights"])
+def test_attention_refuses_what_it_writes_in_other_memory(lib, name, weigh):  # noqa: F811
+    p = ctypes.byref(params(lib))
+    need = (lib.tq_attend_weigh_scratch_bytes(p, 0, B, 4, HKV, 1, CAP) if weigh else
+            lib.tq_attend_shared_scratch_bytes(p, 0, B, 4, HKV, 1, 70, CAP))
+    sizes = ([lib.tq_workspace_bytes(128, 3, 64), 4 * B] + [HKV * 70 * n for n in BYTES[:6]] + SOURCE[:6] +
+             [ROWS, ROWS, need, 4, 4 * B * HKV * CAP])
+    i = A_NAMES.index(name)
+    if name == "weights" and not weigh:
+        return
+    for j, other in enumerate(A_NAMES):
+        unused = other.startswith("prefix") if weigh else other == "weights"
+        if j == i or unused or (name == "out" and other == "q"):
+            continue
+        for off in (0, (sizes[j] - 1) // 16 * 16, -((sizes[i] - 1) // 16 * 16)):
+            at = blocks(sizes)
+            at[i] = at[j] + off
+            assert attend(lib, sizes, at, weigh) == 1, (name, other, off)
