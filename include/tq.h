@@ -370,7 +370,8 @@ tq_status tq_attend_static(const tq_params *p, const float *q, int B, int Hq, in
  * What the call writes (out, scratch, dev_status) may overlap neither what it reads nor one another
  * (TQ_ERR_INVALID_ARG); out may be q.
  * Precision: sums, maxima and normalisers are in 32 bits.  With TQ_F32 every operand of a product
- * keeps 20 bits or more (fp16 pairs hi + lo; fp32 where there is no tensor-core kernel).  With the
+ * keeps 20 bits or more (fp16 pairs hi + lo; fp32 where there is no tensor-core kernel), but for the
+ * 2-bit key centroids of 3-bit parameter sets of TQ_LAW_BETA, 19.  With the
  * 16-bit types operands are rounded to fp16 (relative 2^-11).  A softmax weight (times its value's
  * norm, but for many rows on a prefix) keeps that precision down to 2^-21 of the largest one of the
  * row that a CTA sums it with, and is off by 2^-32 of that at most below (TQ_F32: 20 bits down to 2^-12).
@@ -396,8 +397,9 @@ tq_status tq_attend_shared(const tq_params *p, const void *q, tq_dtype dtype, in
  *   weights : device fp32 [B, Hkv, t_cap].  The call adds to what is there: the caller clears a
  *             token's weight when the token enters the cache
  * The other arguments are those of tq_attend_shared; t_cap >= 1.  In the scores the query rows keep
- * 22 bits whatever dtype is, and the key centroids 20 or more; with the 16-bit types, centroids of
- * 4-bit parameter sets are off by 3.1e-5 of themselves at most.  The rows are added in ascending
+ * 22 bits whatever dtype is, and the key centroids 20 or more (TQ_LAW_BETA, 3-bit sets: 19); with the
+ * 16-bit types, centroids of 4-bit parameter sets are off by 3.1e-5 of themselves at most
+ * (TQ_LAW_BETA: 5e-5).  The rows are added in ascending
  * order: results are bit-identical run to run.
  *   scratch : tq_attend_weigh_scratch_bytes(...) bytes, among them 4 for each (query row, slot)
  * weights counts as written (see tq_attend_shared).

@@ -118,8 +118,9 @@ double off_f16(double v) { return v - (double)__half2float(__float2half_rn((floa
 // A codebook's operand is its centroids over a scale that may be anything, so it is chosen for the
 // centroids to land near fp16 numbers: of 1024 scales that put the largest one on an fp16 number
 // (in [8, 16), so that low halves are normal numbers too), the one with the least squared error by
-// cell mass.  1 bit: exact.  2 bits: one ratio to approximate, about 2^-21 off for the Gaussian law,
-// so that one fp16 operand serves 32-bit scores.  More bits: the error falls by 2 to 4.
+// cell mass.  1 bit: exact.  2 bits: one ratio to approximate, so that one fp16 operand serves 32-bit
+// scores: 2^-21.3 off at most for the Gaussian law; the Beta law has a ratio for each dimension, 2^-19.6
+// off at most for d = 64, 128 and 256, which the tensor-core kernels take.  3 bits: 2^-15 and 2^-14.3.
 double table_scale(const float *c, const float *b, int K, int dim) {
     const int h = K / 2;
     double best = INFINITY, scale = 1.0;

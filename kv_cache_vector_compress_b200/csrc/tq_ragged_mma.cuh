@@ -11,9 +11,9 @@
 // codes are interleaved nibble by nibble.
 //
 // Precision.  A query row is split in two fp16 numbers, hi + lo, in two columns of B, whose sums are
-// added: the scores keep 22 bits of Q, and the key operands are exact to 2^-21 for 1 and 2 bits
-// (ServeTables: a well chosen scale).  For 3 bits they are off by 3e-5 at most, 8e-6 on average, with
-// that scale; F32 adds a second table, which costs as much again as the first.  Value sums: fp16
+// added: the scores keep 22 bits of Q, and the key operands are exact for 1 bit and to 2^-21 for 2 bits
+// (ServeTables: a well chosen scale; the Beta law 2^-19.6).  For 3 bits they are off by 3e-5 at most,
+// 8e-6 on average, with that scale (the Beta law 5e-5 at most); F32 adds a second table, which costs as much again as the first.  Value sums: fp16
 // weights and centroids for 16-bit outputs; F32 splits both.
 //
 // Bound by decoding: its byte permutations and logic run on the ALU pipe, which takes an instruction
