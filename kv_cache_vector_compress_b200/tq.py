@@ -417,6 +417,8 @@ def _row_dtype(dtype: torch.dtype) -> int:
 
 def _arg(t, name: str, dtype: torch.dtype, n: int, dev: int) -> int:
     """The address of t, a contiguous tensor of n values of dtype on CUDA device dev."""
+    if t is None:
+        raise TypeError(f"{name} must be given")
     if t.dtype is dtype and t.numel() == n and t.get_device() == dev and t.is_contiguous():
         return t.data_ptr()
     if t.dtype is not dtype:
@@ -436,6 +438,8 @@ def _device(p: Params, t: torch.Tensor) -> int:
 
 def _cache_args(p: Params, keys, values, n: int, what: str, dev: int):
     """The addresses of a cache of n records (keys: codes, signs, norm, rnorm; values: codes, norm)."""
+    if keys is None or values is None:
+        raise TypeError(f"{what} keys and values must be given")
     kc, ks, kn, kr = keys
     vc, vn = values
     i32, f16 = torch.int32, torch.float16
@@ -533,6 +537,8 @@ def tq_evict(p: Params, keys, values, weights: torch.Tensor, lens: torch.Tensor,
     Entries behind a slice's kept tokens are not written.  tq_attend_weigh adds to the weights, so
     those of tokens still to come have to be zero: they are in an out_weights made here; in one that
     is passed in, the caller clears out_weights[b, :, out_lens[b]:]."""
+    if lens is None:
+        raise TypeError("lens must be given")
     B, dev = lens.numel(), _device(p, lens)
     n, m = B * Hkv * t_cap, B * Hkv * out_cap
     new = lambda *shape, dtype: torch.empty(shape, dtype=dtype, device=lens.device)  # noqa: E731

@@ -159,3 +159,20 @@ def test_out_may_be_the_queries(tq, dtype, d, m):  # noqa: F811
     assert torch.equal(a, pr.shared(tq, out=pr.q))
     pr.q = q.clone()
     assert torch.equal(b, pr.weigh(tq, w2, out=pr.q)) and torch.equal(w1, w2)
+
+
+def test_what_is_missing_is_named(tq):  # noqa: F811
+    import torch
+    pr = Problem(tq, dtype="f16", t_prefix=10, t_cap=20, seed=67)
+    w = torch.from_numpy(pr.w0).cuda()
+    for name, call in [
+            ("lens", lambda: tq.tq_attend_weigh(pr.p, pr.q, pr.k, pr.v, None, 2, 20, w)),
+            ("weights", lambda: tq.tq_attend_weigh(pr.p, pr.q, pr.k, pr.v, pr.dlens, 2, 20, None)),
+            ("own keys", lambda: tq.tq_attend_weigh(pr.p, pr.q, None, pr.v, pr.dlens, 2, 20, w)),
+            ("lens", lambda: tq.tq_attend_shared(pr.p, pr.q, pr.pk, pr.pv, pr.k, pr.v, None, 2, 10, 20)),
+            ("prefix keys", lambda: tq.tq_attend_shared(pr.p, pr.q, None, None, pr.k, pr.v, pr.dlens, 2, 10, 20)),
+            ("own keys", lambda: tq.tq_attend_shared(pr.p, pr.q, pr.pk, pr.pv, None, None, pr.dlens, 2, 10, 20)),
+            ("lens", lambda: tq.tq_evict(pr.p, pr.k, pr.v, w, None, 2, 20, 5, 1, 5)),
+            ("weights", lambda: tq.tq_evict(pr.p, pr.k, pr.v, None, pr.dlens, 2, 20, 5, 1, 5))]:
+        with pytest.raises(TypeError, match=name):
+            call()
