@@ -176,3 +176,16 @@ def test_what_is_missing_is_named(tq):  # noqa: F811
             ("weights", lambda: tq.tq_evict(pr.p, pr.k, pr.v, None, pr.dlens, 2, 20, 5, 1, 5))]:
         with pytest.raises(TypeError, match=name):
             call()
+
+
+@pytest.mark.parametrize("bits,m,serves", [(4, 64, True), (2, 32, True), (3, 0, False), (1, 64, False)])
+def test_tables_are_made_for_sets_that_serve(tq, bits, m, serves):  # noqa: F811
+    """The search of the serving tables takes the host a third of tq_prepare: not done, and their place at the
+    end of the workspace left alone, for a parameter set that the serving calls refuse."""
+    import torch
+    R, S = ref.matrices(128, max(m, 32), 3)
+    p = tq.Params(128, bits, m, torch.from_numpy(R).cuda(), torch.from_numpy(S).cuda() if m else None, prepare=False)
+    p.workspace.fill_(0xAB)
+    tq.tq_prepare(p)
+    assert bool((p.workspace[-256:-144] != 0xAB).any()) == serves
+    assert tq._lib.tq_evict_scratch_bytes(p.ref, 1, 1, 8, 4) == (256 if serves else 0)
