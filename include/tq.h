@@ -350,11 +350,15 @@ tq_status tq_attend_static(const tq_params *p, const float *q, int B, int Hq, in
 /*
  * tq_attend_shared -- attention of a batch whose sequences continue one shared context.
  * (The pages have no counterpart: this is an addition of the library.)
- * The records of the shared prefix are stored once and read once for the whole batch; every
- * sequence's own tokens follow in its own cache, as many as lens says.  With the estimates s_t of
+ * The records of the shared prefix are stored once and read for blocks of query rows, whichever
+ * sequences these are of: 128 rows of the 16-bit types, 4 or 8 with TQ_F32 or up to eight rows in all.
+ * Every sequence's own tokens follow in its own cache, as many as lens says.  With the estimates s_t of
  * tq_scores and the dequantized values v_t of tq_attend,
  *   out = sum_t softmax_t(scale * s_t) v_t  over the prefix and the first lens[b] own tokens.
- * A sequence with nothing to attend gets zeros.
+ * A sequence with nothing to attend gets zeros.  All Nq rows of a sequence attend to all of its
+ * lens[b] tokens: there is no order among them.  Rows that must not see one another's tokens (a draft's,
+ * a prompt's) take calls of their own, each with the lengths of its row.  The norms of the records in use
+ * have to be finite; others make what attends to them NaN or infinite, and no other row.
  *   q        : device [B, Hq, Nq, dim] of dtype: TQ_F16, TQ_BF16 or TQ_F32
  *   t_prefix : tokens of the prefix, >= 0; its arrays hold Hkv * t_prefix records, [Hkv, t_prefix]
  *              (NULL when t_prefix is 0)
@@ -375,6 +379,9 @@ tq_status tq_attend_static(const tq_params *p, const float *q, int B, int Hq, in
  * 16-bit types operands are rounded to fp16 (relative 2^-11).  A softmax weight (times its value's
  * norm, but for many rows on a prefix) keeps that precision down to 2^-21 of the largest one of the
  * row that a CTA sums it with, and is off by 2^-32 of that at most below (TQ_F32: 20 bits down to 2^-12).
+ * The rotated queries are among these operands where more than eight rows (B * Hq/Hkv * Nq) share a
+ * prefix's KV head, and keep 22 bits elsewhere: within that rounding, a request's result depends on how
+ * many others share its call.
  * TQ_ERR_UNSUPPORTED when t_prefix or t_cap exceeds 2^31 - 1024 or B * Hq * Nq exceeds 262140.
  */
 size_t tq_attend_shared_scratch_bytes(const tq_params *p, tq_dtype dtype, int B, int Hq, int Hkv, int Nq,
@@ -396,11 +403,11 @@ tq_status tq_attend_shared(const tq_params *p, const void *q, tq_dtype dtype, in
  *                        for t < lens[b]; entries behind are left as they are
  *   weights : device fp32 [B, Hkv, t_cap].  The call adds to what is there: the caller clears a
  *             token's weight when the token enters the cache
+ * A value norm that is not finite makes the weights of its (sequence, KV head) NaN as well.
  * The other arguments are those of tq_attend_shared; t_cap >= 1.  In the scores the query rows keep
  * 22 bits whatever dtype is, and the key centroids 20 or more (TQ_LAW_BETA, 3-bit sets: 19); with the
  * 16-bit types, centroids of 4-bit parameter sets are off by 3.1e-5 of themselves at most
- * (TQ_LAW_BETA: 5e-5).  The rows are added in ascending
- * order: results are bit-identical run to run.
+ * (TQ_LAW_BETA: 5e-5).  The rows are added in ascending order: results are bit-identical run to run.
  *   scratch : tq_attend_weigh_scratch_bytes(...) bytes, among them 4 for each (query row, slot)
  * weights counts as written (see tq_attend_shared).
  */

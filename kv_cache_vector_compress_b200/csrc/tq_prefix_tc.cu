@@ -85,7 +85,6 @@ struct Cfg {
     static constexpr int KI = TT * G32 / kDecThreads, TP = kDecThreads / G32;  // TP tokens a pass
     static constexpr int SWT = TT * SW;  // sign words of a tile: at most one a thread
     static_assert(KI * TP == TT && SWT <= kDecThreads, "shares");
-    static constexpr int NL = TT / 32;  // norms of a lane in a warp's maximum over the tile
 };
 
 enum Bar { kKFull = 0, kKEmpty = 2, kVFull = 4, kVEmpty = 6, kSFull = 8, kPFull = 10 };

@@ -816,8 +816,9 @@ cudaError_t launch_serve(const ServeCall &call, const ServePlan &plan, void *scr
     pa.len_own = (int32_t *)(base + plan.lens);
     pa.cum_own = (int64_t *)(base + plan.cum);
     pa.dev_status = call.dev_status;
-    // rows that fill the GPU several times over: twice as many a CTA, for half the reads of R (a call
-    // with 2048 rows: 245.1 us with 8 rows a CTA, 243.8 with 16)
+    // Rows that fill the GPU several times over: twice as many a CTA, for half the reads of R.  Whole calls
+    // on a prefix of 64 tokens with 8 against 16 rows a CTA, in us: 2048 rows 31.1 / 28.2 (d = 128), 65.4 /
+    // 60.1 (256), 4096 rows 32.5 / 30.5 (64), 16384 rows 93.9 / 79.8, 148 / 129, 378 / 321.
     const int64_t cols = (P.d + P.m + kPrepCols - 1) / kPrepCols;
     const bool many = call.rows * cols >= 8 * 4 * kSms && P.d <= 256;
     const int prep_rows = many ? 16 : 8;

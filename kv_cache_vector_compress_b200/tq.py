@@ -477,8 +477,9 @@ def tq_attend_shared(p: Params, q: torch.Tensor, prefix_keys, prefix_values, key
                      t_prefix: int, t_cap: int, scale: float = 0.0, out=None, scratch=None, dev_status=None):
     """Attention of q [B, Hq, Nq, dim] (float16, bfloat16 or float32; the output has its type) over a
     compressed prefix that the whole batch shares (records [Hkv, t_prefix]) and the first lens[b]
-    tokens (int32 [B]) of each sequence's own cache (records [B, Hkv, t_cap]).  The prefix tuples are
-    None when t_prefix is 0; the own ones and lens when t_cap is 0."""
+    tokens (int32 [B]) of each sequence's own cache (records [B, Hkv, t_cap]).  All Nq rows of a sequence
+    attend to all of these.  The prefix tuples are None when t_prefix is 0; the own ones and lens when
+    t_cap is 0."""
     B, Hq, Nq, d = q.shape
     dt, dev = _row_dtype(q.dtype), _device(p, q)
     n = B * Hq * Nq * p.dim

@@ -189,3 +189,22 @@ def test_tables_are_made_for_sets_that_serve(tq, bits, m, serves):  # noqa: F811
     tq.tq_prepare(p)
     assert bool((p.workspace[-256:-144] != 0xAB).any()) == serves
     assert tq._lib.tq_evict_scratch_bytes(p.ref, 1, 1, 8, 4) == (256 if serves else 0)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "f32"])
+def test_all_rows_see_all_tokens(tq, dtype):  # noqa: F811
+    """Three rows a sequence in one call: as calls of one row each at the same lengths.  At a row's own
+    lengths those are the causal order, which the one call does not have."""
+    import torch
+    pr = Problem(tq, dtype=dtype, B=3, Hq=4, Hkv=2, Nq=3, t_cap=90, lens=[90, 41, 7], seed=68)
+    w = torch.zeros(3, 2, 90, device="cuda")
+    out, q, tol = pr.weigh(tq, w), pr.q, 2e-3 if dtype == "f16" else 1e-5
+    total = torch.zeros_like(w)
+    for i in range(3):
+        pr.q = q[:, :, i:i + 1].contiguous()
+        one = pr.weigh(tq, total)
+        torch.testing.assert_close(out[:, :, i:i + 1], one, rtol=tol, atol=tol)
+        if i < 2:
+            causal = tq.tq_attend_weigh(pr.p, pr.q, pr.k, pr.v, (pr.dlens - 2 + i).int(), 2, 90, torch.zeros_like(w))
+            assert not torch.allclose(out[:, :, i:i + 1], causal, rtol=tol, atol=tol)
+    torch.testing.assert_close(w, total, rtol=1e-5, atol=1e-6)
