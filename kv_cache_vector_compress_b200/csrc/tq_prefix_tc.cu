@@ -87,7 +87,7 @@ struct Cfg {
     static_assert(KI * TP == TT && SWT <= kDecThreads, "shares");
 };
 
-enum Bar { kKFull = 0, kKEmpty = 2, kVFull = 4, kVEmpty = 6, kSFull = 8, kPFull = 10 };
+enum Bar { kKFull = 0, kKEmpty = 2, kVFull = 4, kVEmpty = 6, kSFull = 8, kPFull = 10, kEnd = 12 };
 
 struct PrefixArgs {
     Prepared P;
@@ -262,6 +262,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(PrefixArgs a) {
             mbar_init(&bars[kSFull + i], 1);
             mbar_init(&bars[kPFull + i], kSmWarps);
         }
+        mbar_init(&bars[kEnd], 1);
         fence_mbar_init();
     }
     if (warp == kSmWarps + kDecWarps) {
@@ -653,6 +654,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(PrefixArgs a) {
             if (lead) mma_commit(&bars[kVEmpty + st]);
             __syncwarp();
             if (C::SB == 1 && j + 1 < nT) ok = scores(j + 1);
+        }
+        if (!ok) {  // gave up: products under way end before the memory that they use is given back
+            if (lead) mma_commit(&bars[kEnd]);
+            __syncwarp();
+            const uint64_t t0 = globaltimer();
+            while (!try_wait8(smem_u32(&bars[kEnd]), 0) && globaltimer() - t0 < kTimeoutNs) {
+            }
         }
     }
     __syncthreads();
