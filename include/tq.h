@@ -351,7 +351,7 @@ tq_status tq_attend_static(const tq_params *p, const float *q, int B, int Hq, in
  * tq_attend_shared -- attention of a batch whose sequences continue one shared context.
  * (The pages have no counterpart: this is an addition of the library.)
  * The records of the shared prefix are stored once and read for blocks of query rows, whichever
- * sequences these are of: 128 rows of the 16-bit types, 4 or 8 with TQ_F32 or up to eight rows in all.
+ * sequences these are of: 128 rows of the 16-bit types where many share it, else 4 or 8.
  * Every sequence's own tokens follow in its own cache, as many as lens says.  With the estimates s_t of
  * tq_scores and the dequantized values v_t of tq_attend,
  *   out = sum_t softmax_t(scale * s_t) v_t  over the prefix and the first lens[b] own tokens.
@@ -379,9 +379,9 @@ tq_status tq_attend_static(const tq_params *p, const float *q, int B, int Hq, in
  * 16-bit types operands are rounded to fp16 (relative 2^-11).  A softmax weight (times its value's
  * norm, but for many rows on a prefix) keeps that precision down to 2^-21 of the largest one of the
  * row that a CTA sums it with, and is off by 2^-32 of that at most below (TQ_F32: 20 bits down to 2^-12).
- * The rotated queries are among these operands where more than eight rows (B * Hq/Hkv * Nq) share a
- * prefix's KV head, and keep 22 bits elsewhere: within that rounding, a request's result depends on how
- * many others share its call.
+ * The rotated queries are among these operands where many rows share a prefix (more than eight of
+ * B * Hq/Hkv * Nq, and with own caches B * Hq * Nq * t_prefix * dim of 40 million or more), and keep 22
+ * bits elsewhere: within that rounding, a request's result depends on how many others share its call.
  * TQ_ERR_UNSUPPORTED when t_prefix or t_cap exceeds 2^31 - 1024 or B * Hq * Nq exceeds 262140.
  */
 size_t tq_attend_shared_scratch_bytes(const tq_params *p, tq_dtype dtype, int B, int Hq, int Hkv, int Nq,

@@ -748,10 +748,14 @@ ServePlan plan_serve(const Prepared &P, tq_dtype dtype, int B, int Hq, int Hkv, 
     p.row_block = kPlRows;
     const int per_sm = p.fast ? ragged_mma_ctas_per_sm(P) : 4;
     // More than eight 16-bit rows on one prefix: the many-row kernel.  Ragged against many-row, 8 KV
-    // heads, 16000 tokens, in us: 8 rows 26.0 / 26.5 (d = 64), 33 / 30 (128), 62 / 54 (256), 12 rows
-    // 31 / 30, 43 / 37, 78 / 62, 64 rows 61 / 34, 93 / 42, 214 / 82; 1000 tokens, 8 rows 15.0 / 17.8,
-    // 20.5 / 18.5, 28.7 / 26.0.  Up to eight the queries keep their 22 bits.
-    const bool tc = p.fast && !f32 && t_prefix > 0 && (int64_t)B * R > 8;
+    // heads, 16000 tokens, in us: 12 rows 30.5 / 23.1 (d = 64), 40.5 / 26.8 (128), 60.0 / 47.3 (256), 64
+    // rows 57.9 / 25.0, 88.1 / 31.0, 289 / 58.6; 1000 tokens, 12 rows 14.4 / 14.6, 17.9 / 15.7, 25.5 / 20.1.
+    // Up to eight the queries keep their 22 bits.  With own caches it is a launch more (6 to 12 us), worth it
+    // from 40 million rows x tokens x coordinates on: 33 million 21.5 / 22.4 (64 rows a head on 1000
+    // tokens, d = 64), 21.7 / 24.8 (32, 1000, 128), 27.5 / 32.3 (16, 1000, 256), 49 million 26.8 / 24.8 (12
+    // of 4 heads, 16000, 64), 27.1 / 25.6 (12, 4000, 128), 65 million 30.5 / 28.1 (64, 1000, 128).
+    const bool tc = p.fast && !f32 && t_prefix > 0 && (int64_t)B * R > 8 &&
+                    (t_cap == 0 || rows * t_prefix >= 40000000 / P.d);
     // the ragged kernel takes both caches in one launch, in blocks of the larger number of rows
     if (p.fast) {
         const bool pre = t_prefix > 0 && !tc;

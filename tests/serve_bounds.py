@@ -40,11 +40,12 @@ def table(bits):
     return {2: 2.0 ** -23, 3: 2.0 ** -19, 4: 5e-5}[bits]
 
 
-def forms(dtype, d, m, B, rows, t_prefix):
+def forms(dtype, d, m, B, Hkv, rows, t_prefix, t_cap):
     """The forms of the prefix's and the own caches' products (the library's choice by sizes)."""
     if d not in (64, 128, 256) or m != d // 2 or dtype == "f32":
         return "f32", "f32"
-    return ("many" if t_prefix and B * rows > 8 else "ragged"), "ragged"
+    many = B * rows > 8 and (t_cap == 0 or B * Hkv * rows * t_prefix >= 40000000 // d)
+    return "many" if many else "ragged", "ragged"
 
 
 def attend(q, R, S, caches, Hkv, scale, bits):

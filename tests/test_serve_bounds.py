@@ -34,9 +34,12 @@ class Host:
         self.pre = ref.Cache(Hkv * t_prefix, d, self.m, bits, seed + 1) if t_prefix else None
         self.own = ref.Cache(B * Hkv * t_cap, d, self.m, bits, seed + 2)
 
+        # (as if the prefix had many rows)
+        self.form = sb.forms(dtype, d, self.m, B, Hkv, Hq // Hkv, t_prefix, 0 if t_prefix else t_cap)
+
     def attend(self, q=None, lens=None, skip=0, no_sign=False):
         """The definition; with other queries or lengths, without the prefix's last `skip` tokens or the signs."""
-        fp, fo = sb.forms(self.dtype, self.d, self.m, self.B, self.Hq // self.Hkv, self.t_prefix)
+        fp, fo = self.form
         caches = []
         if self.pre:
             caches.append((cut(self.pre, self.Hkv, skip, no_sign), self.t_prefix - skip, True, None, fp))
@@ -61,7 +64,7 @@ def cut(c, heads, skip, no_sign):
 
 def emulated(p):
     """The attention with each operand rounded as the kernels round it (the sums in 64 bits)."""
-    form = dict(zip(("pre", "own"), sb.forms(p.dtype, p.d, p.m, p.B, p.Hq // p.Hkv, p.t_prefix)))
+    form = dict(zip(("pre", "own"), p.form))
     eps = 2.0 ** -11
     R, S, G = p.R.astype(np.float64), p.S.astype(np.float64), p.Hq // p.Hkv
     gam, scale = math.sqrt(math.pi / 2) / p.m, 1 / math.sqrt(p.d)

@@ -13,7 +13,7 @@ pytestmark = pytest.mark.gpu
 
 
 def reference(pr):
-    fp, fo = sb.forms(pr.dtype, pr.d, pr.m, pr.B, pr.Hq // pr.Hkv * pr.Nq, pr.t_prefix)
+    fp, fo = sb.forms(pr.dtype, pr.d, pr.m, pr.B, pr.Hkv, pr.Hq // pr.Hkv * pr.Nq, pr.t_prefix, pr.t_cap)
     caches = [(pr.pre, pr.t_prefix, True, None, fp)] if pr.pre else []
     caches += [(pr.own, pr.t_cap, False, pr.lens, fo)] if pr.own else []
     return sb.attend(pr.q64, pr.R, pr.S, caches, pr.Hkv, pr.scale, pr.bits)
@@ -44,7 +44,17 @@ def weigh(tq, **kw):  # noqa: F811
 @pytest.mark.parametrize("bits", [2, 3, 4])
 @pytest.mark.parametrize("B", [5, 16, 33, 70])
 def test_many_rows(tq, d, bits, B):  # noqa: F811
-    shared(tq, dtype="bf16" if B % 2 else "f16", d=d, bits=bits, B=B, Hq=8, Hkv=2, t_prefix=419, t_cap=12, seed=B + d)
+    kw = dict(dtype="bf16" if B % 2 else "f16", d=d, bits=bits, B=B, Hq=8, Hkv=2, seed=B + d)
+    shared(tq, t_prefix=419, t_cap=12, **kw)
+    shared(tq, t_prefix=419, t_cap=0, **kw)
+
+
+@pytest.mark.parametrize("d,B,t_prefix", [(64, 41, 1907), (128, 41, 953), (256, 41, 477), (128, 9, 4341), (256, 70, 1000)])
+@pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
+def test_many_rows_with_own_caches(tq, d, B, t_prefix, dtype):  # noqa: F811
+    """At and past the size from which the prefix and the own caches have kernels of their own, and just below."""
+    for tp in (t_prefix, t_prefix - 2):
+        shared(tq, dtype=dtype, d=d, bits=3, B=B, Hq=8, Hkv=2, t_prefix=tp, t_cap=40, seed=B + d)
 
 
 @pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
@@ -90,6 +100,7 @@ def test_query_sizes(tq, q_scale, dtype):  # noqa: F811
     kw = dict(dtype=dtype, B=9, Hq=8, Hkv=1, t_cap=100, lens=[100] * 9, q_scale=q_scale, seed=7)
     weigh(tq, **kw)
     shared(tq, t_prefix=300, **kw)
+    shared(tq, t_prefix=4400, **kw)
 
 
 @pytest.mark.parametrize("d,bits", [(64, 3), (128, 2), (256, 4), (512, 3)])
@@ -97,7 +108,7 @@ def test_query_sizes(tq, q_scale, dtype):  # noqa: F811
 def test_one_token_takes_it_all(tq, d, bits, dtype):  # noqa: F811
     """Queries of 3e4 along one token's key each: the output is that token's value, its weight one a row."""
     import torch
-    B, Hq, Hkv, tp, cap = 6, 8, 2, 300, 100
+    B, Hq, Hkv, tp, cap = 6, 8, 2, 13100, 100
     pr = Problem(tq, dtype=dtype, d=d, bits=bits, B=B, Hq=Hq, Hkv=Hkv, t_prefix=tp, t_cap=cap, lens=[cap] * B, seed=8)
     R, S, G = pr.R.astype(np.float64), pr.S.astype(np.float64), Hq // Hkv
     rng = np.random.default_rng(9)
@@ -126,7 +137,7 @@ def test_one_token_takes_it_all(tq, d, bits, dtype):  # noqa: F811
                 z = np.sort(z) / math.sqrt(d)
                 assert z[-1] > 1.2 * z[-2] > 0
         pr.q = torch.from_numpy(q).to(pr.q.dtype).cuda()
-        forms = sb.forms(dtype, d, pr.m, B, G, tp)
+        forms = sb.forms(dtype, d, pr.m, B, Hkv, G, tp, cap)
         f = sb.FORMS[forms[0 if use_prefix else 1]]
         err = np.linalg.norm(want, axis=-1) * math.sqrt(f["weight"] ** 2 + f["value"] ** 2 + f["sum"] ** 2)
         hold(pr, pr.shared(tq), want, err, (d, bits, use_prefix))
@@ -136,7 +147,7 @@ def test_one_token_takes_it_all(tq, d, bits, dtype):  # noqa: F811
             np.testing.assert_allclose(w.cpu().numpy(), token, rtol=1e-5, atol=0)
 
 
-@pytest.mark.parametrize("d,bits,B,dtype", [(64, 3, 3, "f32"), (128, 3, 3, "f32"), (128, 4, 3, "f16"), (256, 3, 40, "f16")])
+@pytest.mark.parametrize("d,bits,B,dtype", [(64, 3, 3, "f32"), (128, 3, 3, "f32"), (128, 4, 3, "f16"), (256, 3, 300, "f16")])
 def test_law_of_the_codebook(tq, d, bits, B, dtype):  # noqa: F811
     import oracle
     import torch

@@ -31,7 +31,7 @@ def test_calls_that_follow_on_one_scratch(tq, d, Hq, dtype):  # noqa: F811
     """Calls with other queries and lengths in turn on one scratch, none waited for: each launch of a call
     reads what this call's preparation wrote, never what the call before left in its place."""
     import torch
-    B, Hkv, tp, cap = 24, 2, 900, 300
+    B, Hkv, tp, cap = 24, 2, 4000, 300
     rng = np.random.default_rng(d)
     pr = Problem(tq, dtype=dtype, d=d, B=B, Hq=Hq, Hkv=Hkv, t_prefix=tp, t_cap=cap, seed=72)
     need = max(tq.tq_attend_shared_scratch_bytes(pr.p, pr.q.dtype, B, Hq, Hkv, 1, tp, cap),
