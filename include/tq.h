@@ -358,7 +358,7 @@ tq_status tq_attend_static(const tq_params *p, const float *q, int B, int Hq, in
  * A sequence with nothing to attend gets zeros.  All Nq rows of a sequence attend to all of its
  * lens[b] tokens: there is no order among them.  Rows that must not see one another's tokens (a draft's,
  * a prompt's) take calls of their own, each with the lengths of its row.  The norms of the records in use
- * have to be finite; others make what attends to them NaN or infinite, and no other row.
+ * have to be finite; others can make what attends to them NaN or infinite, and no other row.
  *   q        : device [B, Hq, Nq, dim] of dtype: TQ_F16, TQ_BF16 or TQ_F32
  *   t_prefix : tokens of the prefix, >= 0; its arrays hold Hkv * t_prefix records, [Hkv, t_prefix]
  *              (NULL when t_prefix is 0)
