@@ -2,14 +2,15 @@
 //
 // The rows of all sequences that read a KV head's prefix are one operand: 128 rows at a time are
 // multiplied with tiles of the prefix that are decoded once for them.
-//   S = Q B^T   128 x TT, B = TT tokens x (d + m): ||k|| (c / sigma), then +-||k|| rho, in fp16
+//   S = Q B^T   128 x TT, B = TT tokens x (d + m): c / sigma, then +-rho, in fp16
 //   O += W V    128 x d,  W = the weights in fp16, V = TT tokens x d: ||v|| (c / tau) in fp16
-// The norms are multiplied into the decoded operands (on the FMA pipe, which decoding leaves idle),
-// so that a weight is one fused multiply-add and one exponential of its score.  Both are scaled by
-// powers of two, 2^k and 2^s, one of each a tile, that put the tile's largest norm in [2^10, 2^11):
-// the products stay inside fp16 whatever the norms are.  With z = f 2^-k S and a reference
-// N >= z - s - 15, W = 2^(z - s - N), and the normaliser is 2^s sum W: the partial result
-// (N, l, o) is that of tq_serve.cuh.
+// The key norms multiply the scores in 32 bits.  (In the operands ||k|| rho, rounded to fp16, moved
+// all of a token's signs together: the largest error of the kernel, 7e-4 of the output at 2 bits.)  The
+// value norms are multiplied into the decoded operands (on the FMA pipe, which decoding leaves idle),
+// scaled by a power of two 2^s a tile that puts the tile's largest norm in [2^10, 2^11): the products
+// stay inside fp16 whatever the norms are.  With z = f ||k|| S and a reference N >= z - s - 15,
+// W = 2^(z - s - N), and the normaliser is 2^s sum W: the partial result (N, l, o) is that of
+// tq_serve.cuh.
 //
 // Roles: eight softmax warps (two threads a row, half of a tile's tokens each), eight decoder warps,
 // one warp that issues the MMAs.  The softmax first takes the weights with the reference as it is;
@@ -79,7 +80,8 @@ struct Cfg {
     static constexpr uint32_t NB = (TT + 2) * 2;
     static constexpr uint32_t RS = TT * KWPT * 4, RV = RS + TT * SW * 4, RN = RV + TT * VWPT * 4;
     static constexpr uint32_t RAW = (RN + 3 * NB + 15) / 16 * 16;
-    static constexpr uint32_t OR = (OX + 2 * 128 * 4 + 96 + 15) / 16 * 16;
+    static constexpr uint32_t ON = (OX + 2 * 128 * 4 + 96 + 15) / 16 * 16;  // key norms in fp32, two tiles
+    static constexpr uint32_t OR = ON + 2 * TT * 4;
     static constexpr uint32_t SMEM = OR + 3 * RAW + 1024;  // alignment
     // words of a decoder thread's share of a tile
     static constexpr int KI = TT * G32 / kDecThreads, TP = kDecThreads / G32;  // TP tokens a pass
@@ -319,16 +321,17 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(PrefixArgs a) {
                 ok = false;
             tc_fence_after();
             const uint32_t ts = tl + C::CS + sb * TT;
-            // 2^-k, s and 2^s of the tile
-            const float4 scl = *(const float4 *)(sm + C::OM + vs * 16);
-            const f2 fk = pack2(f * scl.x, f * scl.x);
+            // s and 2^s of the tile, and the key norms of this thread's columns (the same for a whole warp)
+            const float2 scl = *(const float2 *)(sm + C::OM + vs * 16);
+            const float *norms = (const float *)(sm + C::ON) + vs * TT + HC * h;
+            const f2 ff = pack2(f, f);
             // tokens of this thread's columns that are there (the last tile may end early)
             const int cols = T - (j0 + j) * TT - HC * h;
             // the weights, as fp16 pairs, and their sum; returns the largest pair
             uint32_t p[HC / 2];
             f2 sum_w;
             auto weigh = [&]() -> __half2 {
-                const f2 nn = pack2(-(N + scl.y), -(N + scl.y));
+                const f2 nn = pack2(-(N + scl.x), -(N + scl.x));
                 __half2 top = __floats2half2_rn(0.f, 0.f);
                 f2 la = pack2(0.f, 0.f), lb = la;
 #pragma unroll
@@ -338,9 +341,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(PrefixArgs a) {
                     ld_done(s);
                     float e[32];
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) {
-                        unpack2(fma2(pack2(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])), fk, nn), e[2 * k],
-                                e[2 * k + 1]);
+                    for (int k = 0; k < 16; k += 2) {
+                        const ulonglong2 kn = *(const ulonglong2 *)(norms + 32 * c + 2 * k);
+                        unpack2(fma2(pack2(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])), mul2(kn.x, ff), nn),
+                                e[2 * k], e[2 * k + 1]);
+                        unpack2(fma2(pack2(__uint_as_float(s[2 * k + 2]), __uint_as_float(s[2 * k + 3])),
+                                     mul2(kn.y, ff), nn),
+                                e[2 * k + 2], e[2 * k + 3]);
                     }
                     if (cols < HC) {
 #pragma unroll
@@ -380,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(PrefixArgs a) {
                     tmem_ld_wait();
 #pragma unroll
                     for (int k = 0; k < 16; ++k)
-                        if (16 * c + k < cols) mx = fmaxf(mx, __uint_as_float(s[k]) * (f * scl.x) - scl.y);
+                        if (16 * c + k < cols) mx = fmaxf(mx, __uint_as_float(s[k]) * (f * norms[16 * c + k]) - scl.x);
                 }
                 xch[128 * h + r128] = mx;
                 pair_sync();
@@ -409,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(PrefixArgs a) {
                     break;
                 }
             }
-            l2 = fma2(sum_w, pack2(scl.z, scl.z), l2);
+            l2 = fma2(sum_w, pack2(scl.y, scl.y), l2);
 #pragma unroll
             for (int c = 0; c < HC / 32; ++c) {
                 uint32_t v[16];
@@ -534,14 +541,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(PrefixArgs a) {
             live = live && (j < 2 || wait_for(&bars[kKEmpty + st], ((j >> 1) - 1) & 1, abort_s));
             if (!live) return;
             const uint32_t kt = sbase + st * C::KST;
-            // the norms' exponent is field - 15; 2^ke and 2^ve put it at 10
-            const int ke = 25 - top_field(rkn, cnt), ve = 25 - top_field(rvn, cnt);
-            const float kscale = power(ke), vscale = power(ve);
+            // the value norms' exponent is field - 15; 2^ve puts it at 10
+            const int ve = 25 - top_field(rvn, cnt);
+            const float vscale = power(ve);
 #pragma unroll
             for (int i = 0; i < C::KI; ++i) {
-                const int tok = tk + i * C::TP;
-                // a token past the end: the norm is 0, and so is its row
-                const uint32_t nk = pair_of(tok < cnt ? f16_bits_to_f32(rkn[tok]) * kscale : 0.f);
+                const int tok = tk + i * C::TP;  // (past the end: any codes, whose scores are not used)
                 uint32_t w[KB], x[4];
                 read_words<KB>((const uint32_t *)r + tok * C::KWPT + g * KB, w);
                 selectors<KB>(w, x);
@@ -550,12 +555,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(PrefixArgs a) {
                     uint32_t a0, a1, a2, a3;
                     look_up(kh, x[u], 0u, a0, a1);
                     look_up(kh, x[u] >> 16, 0u, a2, a3);
-                    store_scaled(kt + koff[u] + i * C::TP * 128, a0, a1, a2, a3, nk);
+                    store_pairs(kt + koff[u] + i * C::TP * 128, a0, a1, a2, a3);
                 }
             }
             if (dt < C::SWT) {
-                const uint32_t neg =
-                    pair_of(ts < cnt ? -f16_bits_to_f32(rkr[ts]) * (f16_bits_to_f32(rkn[ts]) * kscale) : 0.f);
+                const uint32_t neg = ts < cnt ? (rkr[ts] ^ 0x8000u) * 0x10001u : 0u;  // (-rho, -rho)
                 const uint32_t w = ((const uint32_t *)(r + C::RS))[ts * C::SW + sg];
 #pragma unroll
                 for (int u = 0; u < 4; ++u)
@@ -570,8 +574,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_tc_kernel(PrefixArgs a) {
             live = j < 2 || wait_for(&bars[kVEmpty + st], ((j >> 1) - 1) & 1, abort_s);
             if (!live) return;
             const uint32_t vt = sbase + C::OV + st * C::VST;
-            if (dt == 0)
-                *(float4 *)(sm + C::OM + st * 16) = make_float4(power(-ke), (float)ve, vscale, 0.f);
+            if (dt == 0) *(float2 *)(sm + C::OM + st * 16) = make_float2((float)ve, vscale);
+            if (dt < TT) ((float *)(sm + C::ON))[st * TT + dt] = dt < cnt ? f16_bits_to_f32(rkn[dt]) : 0.f;
 #pragma unroll
             for (int i = 0; i < C::KI; ++i) {
                 const int tok = tk + i * C::TP;

@@ -20,17 +20,17 @@ U32 = 2.0 ** -24
 
 # Errors of one kernel's operands: query and key coordinates, the sign part as a whole, weights, value
 # coordinates; `sum`: of the 32-bit sums and functions, relative to the terms' root of squares.
-#  many: the many-row kernel on a prefix.  Query rows, ||k|| c and ||v|| c rounded to fp16, ||k|| rho too;
-#        the tables' own error 2^-11 at most for 4-bit values, and 2^-14.3 for 3-bit keys
-#  ragged: two fp16 halves of a query; key tables as above (2^-19 up to 2 bits), fp16 values and weights
+#  many: the many-row kernel on a prefix.  Query rows and ||v|| c rounded to fp16
+#  ragged: two fp16 halves of a query; fp16 values and weights
 #  f32: fp16 pairs or fp32 throughout, 2^-20 and better
+# and the fp16 tables of the centroids (keys: 2^-19 up to 2 bits, 5e-5 at 3).
 FORMS = {
-    "many": dict(query=U16, key=lambda bits: math.hypot(U16, table(bits)), sign=U16, weight=U16,
-                 value=math.hypot(U16, 2.0 ** -11), sum=2.0 ** -20),
-    "ragged": dict(query=2.0 ** -22, key=lambda bits: table(bits), sign=0.0, weight=U16, value=2.0 ** -11,
-                   sum=2.0 ** -20),
+    "many": dict(query=U16, key=lambda bits: table(bits), sign=0.0, weight=U16,
+                 value=lambda bits: math.hypot(U16, value_table(bits)), sum=2.0 ** -20),
+    "ragged": dict(query=2.0 ** -22, key=lambda bits: table(bits), sign=0.0, weight=U16,
+                   value=lambda bits: value_table(bits), sum=2.0 ** -20),
     "f32": dict(query=2.0 ** -22, key=lambda bits: 2.0 ** -20 if bits != 3 else 2.0 ** -19, sign=0.0,
-                weight=2.0 ** -20, value=2.0 ** -20, sum=2.0 ** -20),
+                weight=2.0 ** -20, value=lambda bits: 2.0 ** -20, sum=2.0 ** -20),
 }
 SIGMAS = 6.0  # of a normal error: 2e-9 to be beyond, at some 10^6 rows and weights in all
 
@@ -38,6 +38,11 @@ SIGMAS = 6.0  # of a normal error: 2e-9 to be beyond, at some 10^6 rows and weig
 def table(bits):
     """Largest relative error of a key centroid of a `bits`-bit parameter set (the keys' codes have one less)."""
     return {2: 2.0 ** -23, 3: 2.0 ** -19, 4: 5e-5}[bits]
+
+
+def value_table(bits):
+    """Largest relative error of fp16 value centroids of a `bits`-bit parameter set."""
+    return {2: 2.0 ** -19, 3: 5e-5, 4: 2.0 ** -11}[bits]
 
 
 def forms(dtype, d, m, B, Hkv, rows, t_prefix, t_cap):
@@ -84,7 +89,7 @@ def attend(q, R, S, caches, Hkv, scale, bits):
                 # a logit and the exponent it goes into are rounded to fp32 (base 2, with the value's norm)
                 Z.append(var * (kn * scale) ** 2 + (4 * U32 * (np.abs(K[-1]) + 16)) ** 2)
                 V.append(v)
-                EW.append(np.full(n, f["weight"] ** 2 + f["value"] ** 2 + f["sum"] ** 2))
+                EW.append(np.full(n, f["weight"] ** 2 + f["value"](bits) ** 2 + f["sum"] ** 2))
             z, sz2, v, ew = np.concatenate(K, 1), np.concatenate(Z, 1), np.concatenate(V), np.concatenate(EW)
             T = z.shape[1]
             if T == 0:
@@ -112,6 +117,14 @@ def out_of_bounds(got, want, err, half_step):
     if half_step == 2.0 ** -11:
         lim = lim + math.sqrt(d) * 2.0 ** -25  # fp16's smallest numbers
     return ~(off <= lim)
+
+
+def typical(got, want, err, half_step):
+    """Whether the error's root mean square over all rows is that of the model and the output's rounding: of
+    the errors' own size, where out_of_bounds leaves six times that for the worst row."""
+    g = np.asarray(got, np.float64).reshape(want.shape)
+    size = (want ** 2).sum(-1).mean()
+    return ((g - want) ** 2).sum(-1).mean() <= (err ** 2).mean() + half_step ** 2 / 3 * size
 
 
 def weights_out_of_bounds(got, want, werr, before):

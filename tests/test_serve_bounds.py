@@ -62,8 +62,9 @@ def cut(c, heads, skip, no_sign):
     return x
 
 
-def emulated(p):
-    """The attention with each operand rounded as the kernels round it (the sums in 64 bits)."""
+def emulated(p, norms_in_operands=False):
+    """The attention with each operand rounded as the kernels round it (the sums in 64 bits).  Or with the key
+    norms multiplied into the many-row kernel's operands before they are rounded."""
     form = dict(zip(("pre", "own"), p.form))
     eps = 2.0 ** -11
     R, S, G = p.R.astype(np.float64), p.S.astype(np.float64), p.Hq // p.Hkv
@@ -81,8 +82,9 @@ def emulated(p):
                 kc, sg, v = (t[r0:r0 + n] for t in c.dequantized())
                 kn, rho = (t[r0:r0 + n].astype(np.float64) for t in (c.kn, c.kr))
                 if form[name] == "many":
-                    Z.append(scale * (rounded(qr, eps) @ rounded(kn[:, None] * kc, eps).T +
-                                      rounded(qs, eps) @ (sg * rounded(kn * rho, eps)[:, None]).T))
+                    if norms_in_operands:
+                        kc, rho, kn = rounded(kn[:, None] * kc, eps), rounded(kn * rho, eps), 1.0
+                    Z.append(scale * kn * (rounded(qr, eps) @ kc.T + rounded(qs, eps) @ (sg * rho[:, None]).T))
                     V.append(rounded(v, eps))
                 else:
                     Z.append(scale * kn * (qr @ kc.T + qs @ (sg * rho[:, None]).T))
@@ -134,3 +136,22 @@ def test_own_caches(d, bits, dtype):
     for bad in (p.attend(lens=np.maximum(p.lens - 1, 0))[2], 0.75 * w, p.attend(q=rounded(p.q, 2.0 ** -11))[2]):
         if not np.array_equal(bad, w):  # (a 16-bit query is one already)
             assert sb.weights_out_of_bounds(before + bad, w, werr, before).any()
+
+
+@pytest.mark.parametrize("d", [128, 256])
+def test_typical_error_of_many_rows(d):
+    """At 2 bits half of a logit is its sign sketch: ||k|| rho rounded to fp16 moves all of a token's signs
+    together and is the largest error by far.  The key norms stay out of the operands."""
+    p = sketchy(Host("f16", d, 2, 32, 8, 2, 700, 1, lens=[0] * 32, seed=d))
+    want, err, _, _ = p.attend()
+    good, bad = emulated(p), emulated(p, norms_in_operands=True)
+    assert sb.typical(to_type(good, "f16"), want, err, ref.HALF_STEP["f16"])
+    assert not sb.typical(to_type(bad, "f16"), want, err, ref.HALF_STEP["f16"])
+
+
+def sketchy(p):
+    """Norms as 2-bit keys have them: ||k|| near sqrt(d), residuals of 0.6."""
+    rng = np.random.default_rng(5)
+    p.pre.kn[:] = np.sqrt(p.d) * rng.uniform(0.9, 1.1, p.pre.n)
+    p.pre.kr[:] = rng.uniform(0.58, 0.62, p.pre.n)
+    return p

@@ -7,6 +7,7 @@ import pytest
 
 from . import serve_bounds as sb
 from . import serve_ref as ref
+from .test_serve_bounds import sketchy
 from .test_serve_gpu import Problem, tq  # noqa: F401  (tq: the fixture)
 
 pytestmark = pytest.mark.gpu
@@ -47,6 +48,16 @@ def test_many_rows(tq, d, bits, B):  # noqa: F811
     kw = dict(dtype="bf16" if B % 2 else "f16", d=d, bits=bits, B=B, Hq=8, Hkv=2, seed=B + d)
     shared(tq, t_prefix=419, t_cap=12, **kw)
     shared(tq, t_prefix=419, t_cap=0, **kw)
+
+
+@pytest.mark.parametrize("d,bits", [(128, 2), (256, 2), (64, 3), (128, 3), (256, 3)])
+def test_typical_error_of_many_rows(tq, d, bits):  # noqa: F811
+    pr = sketchy(Problem(tq, dtype="f16", d=d, bits=bits, B=32, Hq=8, Hkv=2, t_prefix=700, t_cap=0, seed=d))
+    pr.pk, pr.pv = pr.pre.device()
+    want, err = reference(pr)[:2]
+    out = pr.shared(tq)
+    hold(pr, out, want, err, (d, bits))
+    assert sb.typical(out.double().cpu().numpy(), want, err, ref.HALF_STEP["f16"])
 
 
 @pytest.mark.parametrize("d,B,t_prefix", [(64, 41, 1907), (128, 41, 953), (256, 41, 477), (128, 9, 4341), (256, 70, 1000)])
@@ -139,7 +150,7 @@ def test_one_token_takes_it_all(tq, d, bits, dtype):  # noqa: F811
         pr.q = torch.from_numpy(q).to(pr.q.dtype).cuda()
         forms = sb.forms(dtype, d, pr.m, B, Hkv, G, tp, cap)
         f = sb.FORMS[forms[0 if use_prefix else 1]]
-        err = np.linalg.norm(want, axis=-1) * math.sqrt(f["weight"] ** 2 + f["value"] ** 2 + f["sum"] ** 2)
+        err = np.linalg.norm(want, axis=-1) * math.sqrt(f["weight"] ** 2 + f["value"](bits) ** 2 + f["sum"] ** 2)
         hold(pr, pr.shared(tq), want, err, (d, bits, use_prefix))
         if not use_prefix:
             w = torch.zeros(B, Hkv, cap, device="cuda")
