@@ -34,7 +34,7 @@
 //
 // Bound by the decoders: 128 tokens of d = 128 at 3 bits take them 3200 cycles, the MMAs of the tile
 // 1470, the softmax less than the decoders.  256 rows on each of 8 prefixes of 131072 tokens, d = 128,
-// 3 bits: 190 to 217 us (368 000 cycles), 0.79 to 0.9 PFLOP/s where a large bf16 matrix product measures 1.66.  Sixteen
+// 3 bits: 197 to 217 us (368 000 cycles), 0.79 to 0.87 PFLOP/s where a large bf16 matrix product measures 1.66.  Sixteen
 // decoder warps with registers moved to them from the softmax, and a separate warp for the copies,
 // took as long; there is no room for more registers in flight.
 //
